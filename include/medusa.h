@@ -383,6 +383,98 @@ int medusa_kv_compact_layers(void* k_caches, void* v_caches, int n_layers,
                              int32_t* new_len, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Tree attention with a sliding window and sinks.  medusa_tree_attention
+ * restricted to recent keys: with position p of a prefix slot its index and
+ * of tree node a L_b + depth(a), node i at depth D attends to the keys of
+ * medusa_tree_attention whose position is below `sinks` or above
+ * L_b + D - window (its own position and the window - 1 before it).  The
+ * pages have no counterpart; long contexts are served this way to bound the
+ * cache that a step reads.
+ * window >= 0, 0 = no window (then sinks is ignored); sinks >= 0.  A node
+ * always sees itself.  Layouts, dtypes, limits and errors are those of
+ * medusa_tree_attention.  Slots that some node sees must hold finite values;
+ * all others (slots that have left every window, unused capacity) may hold
+ * anything.  Only the key tiles with a visible slot are read.
+ * A sequence with L_b < 0 or L_b + N > Lcap gets rows of zeros.
+ * bf16 with dh = 128 and (Hq/Hkv) dividing 128 runs on the tcgen05 kernels,
+ * other shapes on a SIMT kernel.  Workspace: the size its own query gives
+ * (it depends on window and sinks), 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+size_t medusa_tree_attention_window_workspace_size(const medusa_tree_t* tree, int B, int Hq,
+                                                   int Hkv, int dh, int Lcap, int dtype,
+                                                   int window, int sinks);
+int medusa_tree_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* prefix_len, const medusa_tree_t* tree, int B,
+                                 int Hq, int Hkv, int dh, int Lcap, float scale, int dtype,
+                                 int window, int sinks, void* out, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache.  A cached row (K or V of one token and kv-head, dh values
+ * x) is dh 4-bit codes, a bf16 scale and an integer zero point:
+ *   lo = min(0, min x), hi = max(0, max x), scale = bf16((hi - lo) / 15),
+ *   zero = clamp(rint(-lo / scale), 0, 15),
+ *   code = clamp(rint(x / scale) + zero, 0, 15),
+ * each step in fp32, rounded to nearest, rint with ties to even; it stands
+ * for scale * (code - zero).  A row of zeros has scale 0.  A row with a NaN,
+ * an infinity or a range above the largest bf16 gets scale NaN.
+ * Layout, all 16-byte aligned:
+ *   *_codes [B][Hkv][Lcap][dh/2] bytes, element 2i in the low half of byte i;
+ *   *_par   [B][Hkv][Lcap][2] bf16: (scale, zero).
+ * dh in {64, 128}; Lcap a multiple of 4.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Stores the rows of new tokens: k, v [B][T][Hkv][dh] of dtype; token t <
+ * count[b] of sequence b goes to slot start[b] + t.  count [B] int32 or NULL
+ * (= T).  Tokens past the count and slots outside [0, Lcap) are skipped:
+ * what the cache holds there stays.  start [B] int32.
+ */
+int medusa_kv_pack(const void* k, const void* v, int dtype, const int32_t* start,
+                   const int32_t* count, int B, int T, int Hkv, int dh, int Lcap, void* k_codes,
+                   void* k_par, void* v_codes, void* v_par, void* stream);
+
+/*
+ * Reads slots start[b] .. start[b] + T - 1 back: k, v [B][T][Hkv][dh] of
+ * dtype (bf16: rounded to nearest).  Zeros where t >= count[b] (count may be
+ * NULL) or the slot is outside [0, Lcap).
+ */
+int medusa_kv_unpack(const void* k_codes, const void* k_par, const void* v_codes,
+                     const void* v_par, const int32_t* start, const int32_t* count, int B, int T,
+                     int Hkv, int dh, int Lcap, int dtype, void* k, void* v, void* stream);
+
+/*
+ * medusa_kv_compact on the 4-bit caches of n_layers layers, one launch.  The
+ * layers' arrays follow one another: *_codes [n_layers][B][Hkv][Lcap][dh/2],
+ * *_par [n_layers][B][Hkv][Lcap][2].  Rows move bit for bit; new_len [B] (may
+ * be NULL) as medusa_kv_compact writes it; same skipped entries.
+ */
+int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_par, int n_layers,
+                             const int32_t* prefix_len, const int32_t* accept_len,
+                             const int32_t* accept_nodes, int B, int Hkv, int dh, int Lcap, int K,
+                             int32_t* new_len, void* stream);
+
+/*
+ * Tree attention over the 4-bit cache: medusa_tree_attention_window (window =
+ * 0: medusa_tree_attention) with k_j and v_j the values the rows stand for.
+ * q, out [B][N][Hq][dh] of dtype; a tree of one node (N = 1) is plain
+ * single-token decoding.  bf16 with dh = 128 runs on a tcgen05 kernel (any
+ * Hq/Hkv), which holds the codes exactly (fp16 code - zero), the softmax
+ * statistics in fp32 and the weights rounded once to fp16; other shapes on a
+ * SIMT kernel in fp32.  A visible row with scale NaN makes its node's output
+ * NaN; slots that no node sees may hold anything.  q finite.
+ */
+size_t medusa_tree_attention_packed_workspace_size(const medusa_tree_t* tree, int B, int Hq,
+                                                   int Hkv, int dh, int Lcap, int dtype,
+                                                   int window, int sinks);
+int medusa_tree_attention_packed(const void* q, const void* k_codes, const void* k_par,
+                                 const void* v_codes, const void* v_par,
+                                 const int32_t* prefix_len, const medusa_tree_t* tree, int B,
+                                 int Hq, int Hkv, int dh, int Lcap, float scale, int dtype,
+                                 int window, int sinks, void* out, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
  * Merge of top-s candidate lists from G vocabulary shards (heads whose W2
  * rows are split across ranks: each rank's medusa_heads_forward top-s over
  * its slice, gathered, then merged).  [MD] "ツリーアテンションによる並列検証":

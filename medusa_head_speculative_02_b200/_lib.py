@@ -56,6 +56,16 @@ SIGNATURES = {
     "medusa_kv_compact": (ci, [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, vp, vp]),
     "medusa_kv_compact_layers": (ci, [vp, vp, ci, C.c_longlong, vp, vp, vp, ci, ci, ci, ci, ci,
                                       ci, vp, vp]),
+    "medusa_tree_attention_window_workspace_size": (csz, [vp, ci, ci, ci, ci, ci, ci, ci, ci]),
+    "medusa_tree_attention_window": (ci, [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, ci, ci,
+                                          vp, vp, csz, vp]),
+    "medusa_tree_attention_packed_workspace_size": (csz, [vp, ci, ci, ci, ci, ci, ci, ci, ci]),
+    "medusa_tree_attention_packed": (ci, [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci,
+                                          ci, ci, vp, vp, csz, vp]),
+    "medusa_kv_pack": (ci, [vp, vp, ci, vp, vp, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp]),
+    "medusa_kv_unpack": (ci, [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, vp, vp, vp]),
+    "medusa_kv_compact_packed": (ci, [vp, vp, vp, vp, ci, vp, vp, vp, ci, ci, ci, ci, ci, vp,
+                                      vp]),
 }
 
 _lib = None

@@ -391,3 +391,196 @@ def medusa_kv_compact(k_cache, v_cache, prefix_len, accept_len, accept_nodes, K:
                                       _dt(k_cache), _ptr(new_len), _stream(k_cache.device)),
             "medusa_kv_compact")
     return new_len
+
+
+# ---------------------------------------------------------------- 4-bit cache, sliding window
+def _same_device(dev, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _i32(t, name: str, shape, dev) -> None:
+    _need(t, name, torch.int32, shape)
+    _same_device(dev, **{name: t})
+
+
+def _out_like(out, name: str, dtype, shape, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, name, dtype, shape)
+    _same_device(dev, **{name: out})
+    return out
+
+
+class PackedCache:
+    """A 4-bit KV cache: codes uint8 [B][Hkv][Lcap][dh/2] and (scale, zero)
+    bf16 [B][Hkv][Lcap][2] of K and V, or with a leading layer axis.  Wraps
+    the caller's tensors; ``PackedCache.empty`` makes zeroed ones (every row
+    then stands for zeros)."""
+
+    __slots__ = ("k_codes", "k_par", "v_codes", "v_par", "layers", "B", "Hkv", "Lcap", "dh",
+                 "device", "_ptrs")
+
+    def __init__(self, k_codes, k_par, v_codes, v_par):
+        _need(k_codes, "k_codes", torch.uint8)
+        shape = tuple(k_codes.shape)
+        if len(shape) not in (4, 5):
+            raise ValueError("k_codes must be [B][Hkv][Lcap][dh/2] or [layers][B][Hkv][Lcap][dh/2]")
+        _need(v_codes, "v_codes", torch.uint8, shape)
+        _need(k_par, "k_par", torch.bfloat16, shape[:-1] + (2,))
+        _need(v_par, "v_par", torch.bfloat16, shape[:-1] + (2,))
+        _same_device(k_codes.device, k_par=k_par, v_codes=v_codes, v_par=v_par)
+        self.k_codes, self.k_par, self.v_codes, self.v_par = k_codes, k_par, v_codes, v_par
+        self.layers = shape[0] if len(shape) == 5 else None
+        self.B, self.Hkv, self.Lcap = shape[-4:-1]
+        self.dh = 2 * shape[-1]
+        self.device = k_codes.device
+        self._ptrs = (_ptr(k_codes), _ptr(k_par), _ptr(v_codes), _ptr(v_par))
+
+    @classmethod
+    def empty(cls, B: int, Hkv: int, Lcap: int, dh: int, device="cuda", layers=None):
+        lead = (B, Hkv, Lcap) if layers is None else (layers, B, Hkv, Lcap)
+        mk = lambda n, dt: torch.zeros(*lead, n, dtype=dt, device=device)  # noqa: E731
+        return cls(mk(dh // 2, torch.uint8), mk(2, torch.bfloat16),
+                   mk(dh // 2, torch.uint8), mk(2, torch.bfloat16))
+
+    def layer(self, i: int) -> "PackedCache":
+        """One layer's cache (a view) of a cache with a layer axis."""
+        if self.layers is None:
+            raise ValueError("the cache has no layer axis")
+        return PackedCache(self.k_codes[i], self.k_par[i], self.v_codes[i], self.v_par[i])
+
+    def _single(self) -> None:
+        if self.layers is not None:
+            raise ValueError("this call takes one layer's cache (cache.layer(i))")
+
+
+def medusa_kv_pack(k, v, cache: PackedCache, start, count=None) -> None:
+    """Stores K/V rows k, v [B][T][Hkv][dh] in the 4-bit cache: token t <
+    count[b] (count None: all T) of sequence b at slot start[b] + t."""
+    cache._single()
+    B, T = k.shape[0], k.shape[1]
+    _need(k, "k", k.dtype, (cache.B, T, cache.Hkv, cache.dh))
+    _need(v, "v", k.dtype, k.shape)
+    dev = cache.device
+    _same_device(dev, k=k, v=v)
+    _i32(start, "start", (B,), dev)
+    if count is not None:
+        _i32(count, "count", (B,), dev)
+    with torch.cuda.device(dev):
+        L.check(L.lib().medusa_kv_pack(_ptr(k), _ptr(v), _dt(k), _ptr(start), _ptr(count), B, T,
+                                       cache.Hkv, cache.dh, cache.Lcap, *cache._ptrs,
+                                       _stream(dev)), "medusa_kv_pack")
+
+
+def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = torch.bfloat16,
+                     count=None, out=None):
+    """The values of slots start[b] .. start[b] + T - 1: (k, v)
+    [B][T][Hkv][dh]; zeros for tokens t >= count[b]."""
+    cache._single()
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    dev = cache.device
+    shape = (cache.B, int(T), cache.Hkv, cache.dh)
+    _i32(start, "start", (cache.B,), dev)
+    if count is not None:
+        _i32(count, "count", (cache.B,), dev)
+    k, v = out if out is not None else (None, None)
+    k, v = _out_like(k, "k", dtype, shape, dev), _out_like(v, "v", dtype, shape, dev)
+    with torch.cuda.device(dev):
+        L.check(L.lib().medusa_kv_unpack(*cache._ptrs, _ptr(start), _ptr(count), cache.B, int(T),
+                                         cache.Hkv, cache.dh, cache.Lcap, _DT[dtype], _ptr(k),
+                                         _ptr(v), _stream(dev)), "medusa_kv_unpack")
+    return k, v
+
+
+def medusa_kv_compact_packed(cache: PackedCache, prefix_len, accept_len, accept_nodes, K: int,
+                             new_len=None):
+    """Compaction of the accepted path in a 4-bit cache (every layer of one
+    with a layer axis, in one launch); returns new_len [B]."""
+    dev = cache.device
+    _i32(prefix_len, "prefix_len", (cache.B,), dev)
+    _i32(accept_len, "accept_len", (cache.B,), dev)
+    _i32(accept_nodes, "accept_nodes", (cache.B, K + 1), dev)
+    new_len = _out_like(new_len, "new_len", torch.int32, (cache.B,), dev)
+    with torch.cuda.device(dev):
+        L.check(L.lib().medusa_kv_compact_packed(
+            *cache._ptrs, 1 if cache.layers is None else cache.layers, _ptr(prefix_len),
+            _ptr(accept_len), _ptr(accept_nodes), cache.B, cache.Hkv, cache.dh, cache.Lcap, K,
+            _ptr(new_len), _stream(dev)), "medusa_kv_compact_packed")
+    return new_len
+
+
+def attention_packed_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
+                                    window: int = 0, sinks: int = 0) -> int:
+    return int(L.lib().medusa_tree_attention_packed_workspace_size(
+        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks))
+
+
+def attention_window_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
+                                    window: int, sinks: int = 0) -> int:
+    return int(L.lib().medusa_tree_attention_window_workspace_size(
+        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks))
+
+
+def _ext_args(q, tree, prefix_len, dev, out, ws, size):
+    """Checked output and workspace of the windowed / 4-bit attention calls
+    (the device is current)."""
+    B, N, Hq, dh = q.shape
+    if N != tree.N:
+        raise ValueError(f"q has {N} nodes, tree has {tree.N}")
+    _i32(prefix_len, "prefix_len", (B,), dev)
+    out = _out_like(out, "out", q.dtype, q.shape, dev)
+    need = size()
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = _ws(need, dev)
+    else:
+        _same_device(dev, ws=ws)
+    return out, ws, ws.numel() * ws.element_size()
+
+
+def medusa_tree_attention_window(q, k_cache, v_cache, prefix_len, tree: Tree, scale: float,
+                                 window: int, sinks: int = 0, out=None, ws=None):
+    """medusa_tree_attention restricted to a sliding window of `window`
+    positions (0: none) and the first `sinks` positions."""
+    B, N, Hq, dh = q.shape
+    Lcap, Hkv = k_cache.shape[1], k_cache.shape[2]
+    dt = _dt(q)
+    dev = q.device
+    _need(q, "q", q.dtype)
+    _need(k_cache, "k_cache", q.dtype, (B, Lcap, Hkv, dh))
+    _need(v_cache, "v_cache", q.dtype, (B, Lcap, Hkv, dh))
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache)
+    with torch.cuda.device(dev):
+        out, ws, nws = _ext_args(q, tree, prefix_len, dev, out, ws,
+                                 lambda: attention_window_workspace_size(
+                                     tree, B, Hq, Hkv, dh, Lcap, q.dtype, window, sinks))
+        L.check(L.lib().medusa_tree_attention_window(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), tree.handle, B, Hq, Hkv, dh,
+            Lcap, float(scale), dt, window, sinks, _ptr(out), _ptr(ws), nws, _stream(dev)),
+            "medusa_tree_attention_window")
+    return out
+
+
+def medusa_tree_attention_packed(q, cache: PackedCache, prefix_len, tree: Tree, scale: float,
+                                 window: int = 0, sinks: int = 0, out=None, ws=None):
+    """Tree attention over a 4-bit cache, full (window 0) or with a sliding
+    window and sinks.  A one-node tree is single-token decoding."""
+    cache._single()
+    B, N, Hq, dh = q.shape
+    dt = _dt(q)
+    dev = q.device
+    _need(q, "q", q.dtype, (cache.B, N, Hq, cache.dh))
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    with torch.cuda.device(dev):
+        out, ws, nws = _ext_args(q, tree, prefix_len, dev, out, ws,
+                                 lambda: attention_packed_workspace_size(
+                                     tree, B, Hq, cache.Hkv, dh, cache.Lcap, q.dtype, window,
+                                     sinks))
+        L.check(L.lib().medusa_tree_attention_packed(
+            _ptr(q), *cache._ptrs, _ptr(prefix_len), tree.handle, B, Hq, cache.Hkv, dh,
+            cache.Lcap, float(scale), dt, window, sinks, _ptr(out), _ptr(ws), nws,
+            _stream(dev)), "medusa_tree_attention_packed")
+    return out

@@ -340,4 +340,25 @@ int attention_launch(const AttnArgs& a, cudaStream_t st) {
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "tree attention launch");
 }
 
+int attention_combine_launch(const AttnArgs& a, const float* po, const float2* pml, int chunks,
+                             cudaStream_t st) {
+  const medusa_tree* t = a.tree;
+  const int R = t->N * (a.Hq / a.Hkv);
+  const int rows = a.B * t->N * a.Hq;
+  cudaError_t e = cudaSuccess;
+#define MEDUSA_COMBINE(T, DH)                                                                     \
+  e = launch_pdl(tree_attn_combine_kernel<T, DH>, dim3((rows + 7) / 8), dim3(256), 0, st, po, pml, \
+                 a.L, a.B, t->N, a.Hq, a.Hkv, a.Lcap, chunks, R, (T*)a.out)
+  if (a.dtype == MEDUSA_F32) {
+    if (a.dh == 64) MEDUSA_COMBINE(float, 64);
+    else MEDUSA_COMBINE(float, 128);
+  } else {
+    if (a.dh == 64) MEDUSA_COMBINE(__nv_bfloat16, 64);
+    else MEDUSA_COMBINE(__nv_bfloat16, 128);
+  }
+#undef MEDUSA_COMBINE
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "tree attention combine launch");
+}
+
 }  // namespace medusa

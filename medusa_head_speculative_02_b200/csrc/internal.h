@@ -157,6 +157,48 @@ TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap);
 int attention_tc_run(const AttnArgs& a, const TcShape& sh, float* po, float2* pml,
                      cudaStream_t st);
 
+// Merges `chunks` partial rows per query row (csrc/attention.cu).
+int attention_combine_launch(const AttnArgs& a, const float* po, const float2* pml, int chunks,
+                             cudaStream_t st);
+
+// ---------------------------------------------------------------- 4-bit cache
+// Device pointers of a 4-bit cache (csrc/kv_pack.cu has the row format).
+struct PackedCache {
+  void* k_codes;
+  void* k_par;
+  void* v_codes;
+  void* v_par;
+  int Hkv, dh, Lcap;
+};
+struct PackedRows {
+  const void* k;  // values to store (kv_pack)
+  const void* v;
+  void* k_out;    // values read back (kv_unpack)
+  void* v_out;
+  const int32_t* start;
+  const int32_t* count;  // null: every sequence has T tokens
+  int B, T, dtype;
+  PackedCache c;
+};
+int kv_pack_launch(const PackedRows& a, cudaStream_t st);
+int kv_unpack_launch(const PackedRows& a, cudaStream_t st);
+int kv_compact_packed_launch(const PackedCache& c, int layers, int B, const int32_t* L,
+                             const int32_t* alen, const int32_t* anodes, int K, int32_t* new_len,
+                             cudaStream_t st);
+
+// Tree attention over the 4-bit cache (packed != null; a.k and a.v unused)
+// and / or with a sliding window (window > 0).
+struct AttnExtArgs {
+  AttnArgs a;
+  int window, sinks;
+  const PackedCache* packed;
+};
+// Most slots a sequence's nodes can see.
+long long ext_max_keys(int Lcap, int N, int window, int sinks);
+size_t attention_ext_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
+                               int dtype, int window, int sinks, bool packed);
+int attention_ext_launch(const AttnExtArgs& x, cudaStream_t st);
+
 // ---------------------------------------------------------------- acceptance
 struct AcceptArgs {
   const void* vlog;

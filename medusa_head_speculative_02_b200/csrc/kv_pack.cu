@@ -1,0 +1,337 @@
+// The 4-bit KV cache: storing K/V rows, reading them back, and the compaction
+// of the accepted path.
+//
+// A cached row (one token's K or V of one kv-head, dh values x) is held as
+// dh 4-bit codes, a bf16 scale and an integer zero point:
+//   lo = min(0, min x), hi = max(0, max x)
+//   scale = bf16((hi - lo) / 15)
+//   zero  = clamp(rint(-lo / scale), 0, 15)
+//   code  = clamp(rint(x / scale) + zero, 0, 15)
+// and stands for scale * (code - zero).  Every step is an fp32 operation
+// rounded to nearest, rint rounds ties to even, so the codes are defined to
+// the last bit.  The range always holds 0, hence 0 is stored exactly, and
+// code - zero is a small integer, exact in every type the readers use.  A
+// row of zeros has scale 0; a row with a NaN, an infinity or a range beyond
+// bf16 gets a NaN scale (it reads back as NaN).
+//
+// Layout: codes [B][Hkv][Lcap][dh/2] bytes (element 2i in the low half of byte
+// i), (scale, zero) [B][Hkv][Lcap] bf16 pairs: the keys of one kv-head are
+// contiguous, so a 128-key tile is one 8 KB block (dh = 128) and its scales
+// 512 bytes.  68 bytes per row of 128 values, 3.8 x less than bf16.
+//
+// All three kernels move bytes (HBM- or latency-bound).  A row is taken by
+// dh/8 lanes of a warp, 8 values (one 32-bit code word) each, so loads of
+// values are 16 or 32 bytes per lane and coalesced along the heads.
+#include "common.cuh"
+#include "internal.h"
+
+namespace medusa {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 consecutive values of a row as fp32.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  __align__(16) __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+
+// rint(x / s) as the correctly rounded fp32 quotient gives it, r = 1 / s.
+// x * r is within 2e-6 of the quotient (|x / s| <= 16), so its rounding
+// decides unless it lies that close to a tie; only then is the division done.
+__device__ __forceinline__ float rint_div(float x, float s, float r) {
+  const float q = x * r;
+  const float n = rintf(q);
+  if (fabsf(fabsf(q - n) - 0.5f) > 1e-5f) return n;
+  return rintf(__fdiv_rn(x, s));
+}
+
+// Encodes one row held 8 values to a lane by LPR neighbouring lanes: this
+// lane's code word, and the row's (scale, zero) word.
+template <int LPR>
+__device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
+  float lo = 0.f, hi = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+    bad |= !(fabsf(x[i]) <= 3.4028234e38f);  // NaN or infinity
+  }
+  if (bad) hi = INFINITY;  // reaches every lane through the row maximum
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  const float s = __bfloat162float(sb);
+  if (!(s <= 3.4028234e38f)) {
+    par = 0x7fc0u;  // scale NaN, zero 0
+    return 0u;
+  }
+  if (s == 0.f) {
+    par = 0u;
+    return 0u;
+  }
+  float zero;
+  uint32_t w = 0u;
+  if (s < 1e-30f) {  // 1 / s may overflow: divide
+    zero = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + zero, 0.f), 15.f);
+      w |= (uint32_t)(int)c << (4 * i);
+    }
+  } else {
+    const float r = __frcp_rn(s);
+    zero = fminf(fmaxf(rint_div(-lo, s, r), 0.f), 15.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = fminf(fmaxf(rint_div(x[i], s, r) + zero, 0.f), 15.f);
+      w |= (uint32_t)(int)c << (4 * i);
+    }
+  }
+  par = (uint32_t)__bfloat16_as_ushort(sb) |
+        ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(zero)) << 16);
+  return w;
+}
+
+// (b, t, h) of row `row` of [B][T][H], and the cache row it goes to (or -1:
+// not one of the sequence's tokens, or outside the cache).
+__device__ __forceinline__ long long cache_row(long long row, int T, int H, int Lcap,
+                                               const int32_t* __restrict__ start,
+                                               const int32_t* __restrict__ count) {
+  const long long bt = row / H;
+  const int h = (int)(row - bt * H);
+  const long long b = bt / T;
+  const int t = (int)(bt - b * T);
+  if (count != nullptr && t >= count[b]) return -1;
+  const long long slot = (long long)start[b] + t;
+  if (slot < 0 || slot >= Lcap) return -1;
+  return (b * H + h) * Lcap + slot;
+}
+
+// Rows [B][T][H] of K (grid y 0) and V (grid y 1); RPT rows per lane group in
+// flight at once.
+template <typename T, int DH, int RPT>
+__global__ void __launch_bounds__(kThreads)
+    kv_pack_kernel(const T* __restrict__ k, const T* __restrict__ v,
+                   const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+                   long long rows, int Tn, int H, int Lcap, uint32_t* __restrict__ kc,
+                   uint32_t* __restrict__ kp, uint32_t* __restrict__ vc,
+                   uint32_t* __restrict__ vp) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int LPR = DH / 8;
+  constexpr int GROUPS = kThreads / LPR;
+  const T* __restrict__ src = blockIdx.y ? v : k;
+  uint32_t* __restrict__ codes = blockIdx.y ? vc : kc;
+  uint32_t* __restrict__ par = blockIdx.y ? vp : kp;
+  const int sub = threadIdx.x % LPR;
+  const long long row0 = (long long)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+  float x[RPT][8];
+  long long dst[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const long long row = row0 + (long long)i * GROUPS;
+    dst[i] = row < rows ? cache_row(row, Tn, H, Lcap, start, count) : -1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+    if (dst[i] >= 0) load8(src + row * DH + sub * 8, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    uint32_t p;
+    const uint32_t w = encode<LPR>(x[i], p);  // every lane: the row maxima are shuffles
+    if (dst[i] >= 0) {
+      codes[dst[i] * LPR + sub] = w;
+      if (sub == 0) par[dst[i]] = p;
+    }
+  }
+}
+
+// The values of slots start_b .. start_b + T - 1; zeros past a sequence's
+// count and outside the cache.
+template <typename T, int DH, int RPT>
+__global__ void __launch_bounds__(kThreads)
+    kv_unpack_kernel(const uint32_t* __restrict__ kc, const uint32_t* __restrict__ kp,
+                     const uint32_t* __restrict__ vc, const uint32_t* __restrict__ vp,
+                     const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+                     long long rows, int Tn, int H, int Lcap, T* __restrict__ k,
+                     T* __restrict__ v) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int LPR = DH / 8;
+  constexpr int GROUPS = kThreads / LPR;
+  const uint32_t* __restrict__ codes = blockIdx.y ? vc : kc;
+  const uint32_t* __restrict__ par = blockIdx.y ? vp : kp;
+  T* __restrict__ out = blockIdx.y ? v : k;
+  const int sub = threadIdx.x % LPR;
+  const long long row0 = (long long)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+  uint32_t w[RPT], p[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const long long row = row0 + (long long)i * GROUPS;
+    const long long src = row < rows ? cache_row(row, Tn, H, Lcap, start, count) : -1;
+    w[i] = src >= 0 ? codes[src * LPR + sub] : 0u;
+    p[i] = src >= 0 ? par[src] : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const long long row = row0 + (long long)i * GROUPS;
+    if (row >= rows) continue;
+    const float s = __uint_as_float(p[i] << 16), z = __uint_as_float(p[i] & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s * ((float)((w[i] >> (4 * e)) & 15u) - z);
+    store8(out + row * DH + sub * 8, x);
+  }
+}
+
+// Accepted path of every (layer, sequence, kv-head): slot L_b + j <- slot
+// L_b + n_j, j = 1..a.  A thread owns one 32-bit word of a slot (code words
+// of K and V, then the two (scale, zero) words) and reads all its sources
+// before it writes: n_j >= j, so no source is overwritten by an earlier move
+// and the moves are those of the in-order copy.
+__global__ void __launch_bounds__(kThreads)
+    kv_compact_packed_kernel(uint32_t* __restrict__ kc, uint32_t* __restrict__ kp,
+                             uint32_t* __restrict__ vc, uint32_t* __restrict__ vp,
+                             const int32_t* __restrict__ L, const int32_t* __restrict__ alen,
+                             const int32_t* __restrict__ anodes, long long total, int B, int H,
+                             int words, int Lcap, int K, int32_t* __restrict__ new_len) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i < B && new_len != nullptr) {
+    const int a = alen[i], Lb = L[i];
+    new_len[i] = (a >= 0 && a <= K && Lb >= 0) ? Lb + 1 + a : -1;
+  }
+  if (i >= total) return;
+  const int per = 2 * words + 2;
+  const long long lbh = i / per;  // (layer, sequence, kv-head)
+  const int w = (int)(i - lbh * per);
+  const int b = (int)((lbh / H) % B);
+  const int a = alen[b], Lb = L[b];
+  if (a < 0 || a > K || Lb < 0) return;
+  // word w of a slot: K codes, V codes, K (scale, zero), V (scale, zero)
+  uint32_t* base;
+  int stride;
+  if (w < 2 * words) {
+    base = (w < words ? kc : vc) + lbh * Lcap * words + (w < words ? w : w - words);
+    stride = words;
+  } else {
+    base = (w == 2 * words ? kp : vp) + lbh * Lcap;
+    stride = 1;
+  }
+  uint32_t val[MEDUSA_MAX_K];
+  bool ok[MEDUSA_MAX_K];
+#pragma unroll
+  for (int j = 1; j <= MEDUSA_MAX_K; ++j) {
+    ok[j - 1] = false;
+    if (j <= a) {
+      const int n = anodes[(size_t)b * (K + 1) + j];
+      const long long src = (long long)Lb + n;
+      ok[j - 1] = n >= j && src < Lcap && (long long)Lb + j < Lcap;
+      if (w == 0) dbg_ok(ok[j - 1], DBG_COMPACT_NODE);
+      if (ok[j - 1]) val[j - 1] = base[src * stride];
+    }
+  }
+#pragma unroll
+  for (int j = 1; j <= MEDUSA_MAX_K; ++j)
+    if (ok[j - 1]) base[((long long)Lb + j) * stride] = val[j - 1];
+}
+
+int grid_of(long long rows, int per_block, unsigned* g) {
+  const long long n = (rows + per_block - 1) / per_block;
+  if (n > 0x7fffffffLL) return fail(MEDUSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  *g = (unsigned)n;
+  return MEDUSA_OK;
+}
+
+// Few rows: one per lane group (latency); many: four in flight.
+template <typename T, int DH>
+int pack_launch_t(const PackedRows& a, cudaStream_t st) {
+  const long long rows = (long long)a.B * a.T * a.c.Hkv;
+  constexpr int GROUPS = kThreads / (DH / 8);
+  const bool many = rows >= 4LL * GROUPS * num_sms();
+  unsigned g;
+  int rc = grid_of(rows, GROUPS * (many ? 4 : 1), &g);
+  if (rc) return rc;
+  auto* fn = many ? kv_pack_kernel<T, DH, 4> : kv_pack_kernel<T, DH, 1>;
+  cudaError_t e = launch_pdl(fn, dim3(g, 2), dim3(kThreads), 0, st, (const T*)a.k, (const T*)a.v,
+                             a.start, a.count, rows, a.T, a.c.Hkv, a.c.Lcap, (uint32_t*)a.c.k_codes,
+                             (uint32_t*)a.c.k_par, (uint32_t*)a.c.v_codes, (uint32_t*)a.c.v_par);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "kv_pack_kernel launch");
+}
+template <typename T, int DH>
+int unpack_launch_t(const PackedRows& a, cudaStream_t st) {
+  const long long rows = (long long)a.B * a.T * a.c.Hkv;
+  constexpr int GROUPS = kThreads / (DH / 8);
+  const bool many = rows >= 4LL * GROUPS * num_sms();
+  unsigned g;
+  int rc = grid_of(rows, GROUPS * (many ? 4 : 1), &g);
+  if (rc) return rc;
+  auto* fn = many ? kv_unpack_kernel<T, DH, 4> : kv_unpack_kernel<T, DH, 1>;
+  cudaError_t e = launch_pdl(fn, dim3(g, 2), dim3(kThreads), 0, st, (const uint32_t*)a.c.k_codes,
+                             (const uint32_t*)a.c.k_par, (const uint32_t*)a.c.v_codes,
+                             (const uint32_t*)a.c.v_par, a.start, a.count, rows, a.T, a.c.Hkv,
+                             a.c.Lcap, (T*)a.k_out, (T*)a.v_out);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "kv_unpack_kernel launch");
+}
+
+}  // namespace
+
+int kv_pack_launch(const PackedRows& a, cudaStream_t st) {
+  if (a.dtype == MEDUSA_F32)
+    return a.c.dh == 64 ? pack_launch_t<float, 64>(a, st) : pack_launch_t<float, 128>(a, st);
+  return a.c.dh == 64 ? pack_launch_t<__nv_bfloat16, 64>(a, st)
+                      : pack_launch_t<__nv_bfloat16, 128>(a, st);
+}
+
+int kv_unpack_launch(const PackedRows& a, cudaStream_t st) {
+  if (a.dtype == MEDUSA_F32)
+    return a.c.dh == 64 ? unpack_launch_t<float, 64>(a, st) : unpack_launch_t<float, 128>(a, st);
+  return a.c.dh == 64 ? unpack_launch_t<__nv_bfloat16, 64>(a, st)
+                      : unpack_launch_t<__nv_bfloat16, 128>(a, st);
+}
+
+int kv_compact_packed_launch(const PackedCache& c, int layers, int B, const int32_t* L,
+                             const int32_t* alen, const int32_t* anodes, int K, int32_t* new_len,
+                             cudaStream_t st) {
+  const int words = c.dh / 8;
+  const long long total = (long long)layers * B * c.Hkv * (2 * words + 2);
+  unsigned g;
+  int rc = grid_of(total > B ? total : B, kThreads, &g);
+  if (rc) return rc;
+  cudaError_t e = launch_pdl(kv_compact_packed_kernel, dim3(g), dim3(kThreads), 0, st,
+                             (uint32_t*)c.k_codes, (uint32_t*)c.k_par, (uint32_t*)c.v_codes,
+                             (uint32_t*)c.v_par, L, alen, anodes, total, B, c.Hkv, words, c.Lcap,
+                             K, new_len);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "kv_compact_packed_kernel launch");
+}
+
+}  // namespace medusa

@@ -636,6 +636,166 @@ int medusa_kv_compact_layers(void* k_caches, void* v_caches, int n_layers,
                            n_layers > 1 ? layer_stride : 0);
 }
 
+namespace {
+
+// Shared argument checks of the windowed / 4-bit attention calls; the tree is
+// checked by the caller.
+int check_attention_ext(const medusa_tree_t* tree, int B, int Hq, int Hkv, int dh, int Lcap,
+                        int dtype, int window, int sinks, bool packed) {
+  if (!tree) return fail(MEDUSA_ERR_INVALID_ARG, "tree is NULL");
+  if (!dtype_ok(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "bad dtype");
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+    return fail(MEDUSA_ERR_INVALID_ARG, "need Hq % Hkv == 0 and positive head counts");
+  if (dh != 64 && dh != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "dh must be 64 or 128");
+  if (Lcap < tree->N) return fail(MEDUSA_ERR_INVALID_ARG, "Lcap < N");
+  if (packed && Lcap % 4) return fail(MEDUSA_ERR_UNSUPPORTED, "4-bit cache: Lcap must be a multiple of 4");
+  if (window < 0 || sinks < 0) return fail(MEDUSA_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  // query rows of the call, and of one kv-head's partial rows, in 31 bits
+  if ((long long)B * tree->N * Hq > 0x7fffffffLL)
+    return fail(MEDUSA_ERR_UNSUPPORTED, "more than 2^31 - 1 query rows");
+  return MEDUSA_OK;
+}
+
+int check_packed(const void* k_codes, const void* k_par, const void* v_codes, const void* v_par) {
+  if (!k_codes || !k_par || !v_codes || !v_par) return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(k_codes) || !aligned16(k_par) || !aligned16(v_codes) || !aligned16(v_par))
+    return fail(MEDUSA_ERR_INVALID_ARG, "4-bit cache arrays must be 16-byte aligned");
+  return MEDUSA_OK;
+}
+
+int check_packed_shape(int B, int T, int Hkv, int dh, int Lcap) {
+  if (B < 0 || T < 0 || Hkv <= 0 || Lcap <= 0) return fail(MEDUSA_ERR_INVALID_ARG, "bad shape");
+  if (dh != 64 && dh != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "dh must be 64 or 128");
+  if (Lcap % 4) return fail(MEDUSA_ERR_UNSUPPORTED, "4-bit cache: Lcap must be a multiple of 4");
+  return MEDUSA_OK;
+}
+
+int attention_ext_call(const void* q, const void* k, const void* v, const PackedCache* packed,
+                       const int32_t* prefix_len, const medusa_tree_t* tree, int B, int Hq,
+                       int Hkv, int dh, int Lcap, float scale, int dtype, int window, int sinks,
+                       void* out, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_tree(tree);
+  if (rc) return rc;
+  rc = check_attention_ext(tree, B, Hq, Hkv, dh, Lcap, dtype, window, sinks, packed != nullptr);
+  if (rc) return rc;
+  if (!(std::isfinite(scale) && scale > 0.f))
+    return fail(MEDUSA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (B == 0) return MEDUSA_OK;
+  if (!q || !prefix_len || !out) return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+  if (packed) {
+    rc = check_packed(packed->k_codes, packed->k_par, packed->v_codes, packed->v_par);
+    if (rc) return rc;
+  } else {
+    if (!k || !v) return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned16(k) || !aligned16(v))
+      return fail(MEDUSA_ERR_INVALID_ARG, "k_cache and v_cache must be 16-byte aligned");
+  }
+  if (!aligned16(q) || !aligned16(out))
+    return fail(MEDUSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (window == 0) sinks = 0;
+  const size_t need =
+      attention_ext_workspace(tree, B, Hq, Hkv, dh, Lcap, dtype, window, sinks, packed != nullptr);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
+    return fail(MEDUSA_ERR_INVALID_ARG, "workspace too small or not 16-byte aligned");
+  AttnExtArgs x{{q, k, v, prefix_len, tree, B, Hq, Hkv, dh, Lcap, scale, dtype, out, ws, ws_bytes},
+                window, sinks, packed};
+  return attention_ext_launch(x, (cudaStream_t)stream);
+}
+
+}  // namespace
+
+size_t medusa_tree_attention_window_workspace_size(const medusa_tree_t* tree, int B, int Hq,
+                                                   int Hkv, int dh, int Lcap, int dtype,
+                                                   int window, int sinks) {
+  if (check_attention_ext(tree, B, Hq, Hkv, dh, Lcap, dtype, window, sinks, false)) return 0;
+  return attention_ext_workspace(tree, B, Hq, Hkv, dh, Lcap, dtype, window, window ? sinks : 0, false);
+}
+
+int medusa_tree_attention_window(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* prefix_len, const medusa_tree_t* tree, int B,
+                                 int Hq, int Hkv, int dh, int Lcap, float scale, int dtype,
+                                 int window, int sinks, void* out, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  medusa::NvtxRange nvtx_range("medusa_tree_attention_window");
+  return attention_ext_call(q, k_cache, v_cache, nullptr, prefix_len, tree, B, Hq, Hkv, dh, Lcap,
+                            scale, dtype, window, sinks, out, ws, ws_bytes, stream);
+}
+
+size_t medusa_tree_attention_packed_workspace_size(const medusa_tree_t* tree, int B, int Hq,
+                                                   int Hkv, int dh, int Lcap, int dtype,
+                                                   int window, int sinks) {
+  if (check_attention_ext(tree, B, Hq, Hkv, dh, Lcap, dtype, window, sinks, true)) return 0;
+  return attention_ext_workspace(tree, B, Hq, Hkv, dh, Lcap, dtype, window, window ? sinks : 0, true);
+}
+
+int medusa_tree_attention_packed(const void* q, const void* k_codes, const void* k_par,
+                                 const void* v_codes, const void* v_par,
+                                 const int32_t* prefix_len, const medusa_tree_t* tree, int B,
+                                 int Hq, int Hkv, int dh, int Lcap, float scale, int dtype,
+                                 int window, int sinks, void* out, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  medusa::NvtxRange nvtx_range("medusa_tree_attention_packed");
+  const PackedCache c{const_cast<void*>(k_codes), const_cast<void*>(k_par),
+                      const_cast<void*>(v_codes), const_cast<void*>(v_par), Hkv, dh, Lcap};
+  return attention_ext_call(q, nullptr, nullptr, &c, prefix_len, tree, B, Hq, Hkv, dh, Lcap, scale,
+                            dtype, window, sinks, out, ws, ws_bytes, stream);
+}
+
+int medusa_kv_pack(const void* k, const void* v, int dtype, const int32_t* start,
+                   const int32_t* count, int B, int T, int Hkv, int dh, int Lcap, void* k_codes,
+                   void* k_par, void* v_codes, void* v_par, void* stream) {
+  medusa::NvtxRange nvtx_range("medusa_kv_pack");
+  if (!dtype_ok(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "bad dtype");
+  int rc = check_packed_shape(B, T, Hkv, dh, Lcap);
+  if (rc) return rc;
+  if (B == 0 || T == 0) return MEDUSA_OK;
+  if (!k || !v || !start) return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(k) || !aligned16(v))
+    return fail(MEDUSA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  rc = check_packed(k_codes, k_par, v_codes, v_par);
+  if (rc) return rc;
+  return kv_pack_launch({k, v, nullptr, nullptr, start, count, B, T, dtype,
+                         {k_codes, k_par, v_codes, v_par, Hkv, dh, Lcap}},
+                        (cudaStream_t)stream);
+}
+
+int medusa_kv_unpack(const void* k_codes, const void* k_par, const void* v_codes,
+                     const void* v_par, const int32_t* start, const int32_t* count, int B, int T,
+                     int Hkv, int dh, int Lcap, int dtype, void* k, void* v, void* stream) {
+  medusa::NvtxRange nvtx_range("medusa_kv_unpack");
+  if (!dtype_ok(dtype)) return fail(MEDUSA_ERR_INVALID_ARG, "bad dtype");
+  int rc = check_packed_shape(B, T, Hkv, dh, Lcap);
+  if (rc) return rc;
+  if (B == 0 || T == 0) return MEDUSA_OK;
+  if (!k || !v || !start) return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(k) || !aligned16(v))
+    return fail(MEDUSA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  rc = check_packed(k_codes, k_par, v_codes, v_par);
+  if (rc) return rc;
+  return kv_unpack_launch({nullptr, nullptr, k, v, start, count, B, T, dtype,
+                           {const_cast<void*>(k_codes), const_cast<void*>(k_par),
+                            const_cast<void*>(v_codes), const_cast<void*>(v_par), Hkv, dh, Lcap}},
+                          (cudaStream_t)stream);
+}
+
+int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_par, int n_layers,
+                             const int32_t* prefix_len, const int32_t* accept_len,
+                             const int32_t* accept_nodes, int B, int Hkv, int dh, int Lcap, int K,
+                             int32_t* new_len, void* stream) {
+  medusa::NvtxRange nvtx_range("medusa_kv_compact_packed");
+  int rc = check_packed_shape(B, 0, Hkv, dh, Lcap);
+  if (rc) return rc;
+  if (n_layers < 0 || K < 0 || K > MEDUSA_MAX_K) return fail(MEDUSA_ERR_INVALID_ARG, "bad shape");
+  if (B == 0 || n_layers == 0) return MEDUSA_OK;
+  if (!prefix_len || !accept_len || !accept_nodes)
+    return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
+  rc = check_packed(k_codes, k_par, v_codes, v_par);
+  if (rc) return rc;
+  return kv_compact_packed_launch({k_codes, k_par, v_codes, v_par, Hkv, dh, Lcap}, n_layers, B,
+                                  prefix_len, accept_len, accept_nodes, K, new_len,
+                                  (cudaStream_t)stream);
+}
+
 int medusa_topk_merge(const float* val, const int32_t* idx, long long shard_stride,
                       const int32_t* v0, int G, int R, int c, int s, int32_t* out_idx,
                       float* out_val, void* stream) {
