@@ -303,7 +303,7 @@ int simt_run(const SimtParams& p, int RB, long long ctas, cudaStream_t st) {
 int simt_launch(const AttnExtArgs& x, cudaStream_t st) {
   const AttnArgs& a = x.a;
   const medusa_tree* t = a.tree;
-  const SimtPlan pl = simt_plan(t, a.B, a.Hq, a.Hkv, a.dh, a.Lcap, x.window, x.sinks);
+  const SimtPlan pl = simt_plan(t, a.B, a.Hq, a.Hkv, a.dh, a.Lcap, a.window, a.sinks);
   if (pl.ctas > 0x7fffffffLL) return fail(MEDUSA_ERR_UNSUPPORTED, "too many query rows for one launch");
   SimtParams p;
   p.q = a.q;
@@ -323,8 +323,8 @@ int simt_launch(const AttnExtArgs& x, cudaStream_t st) {
   p.R = pl.R;
   p.rblocks = pl.rblocks;
   p.P = pl.P;
-  p.window = x.window;
-  p.sinks = x.sinks;
+  p.window = a.window;
+  p.sinks = a.sinks;
   p.qscale = a.scale * kLog2e;
   p.po = (float*)((uint8_t*)a.ws + pl.off_o);
   p.pml = (float2*)((uint8_t*)a.ws + pl.off_ml);
@@ -352,14 +352,53 @@ long long ext_max_keys(int Lcap, int N, int window, int sinks) {
   return k < Lcap ? k : Lcap;
 }
 
+namespace {
+
+// Windowed bf16 path: the launch shape is the plain kernels' for a cache that
+// holds what a sequence's nodes can see, whole tiles for the sinks.
+int window_tc_lcap(int Lcap, int N, int window, int sinks) {
+  const long long s = ((long long)sinks + 127) / 128 * 128;
+  const long long k = ext_max_keys(Lcap, N, window, (int)(s < 0x7fffffff ? s : 0x7fffffff));
+  return (int)k;
+}
+struct WindowTcPlan {
+  TcShape sh;
+  size_t off_o, off_ml, total;
+};
+WindowTcPlan window_tc_plan(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
+                            int window, int sinks) {
+  WindowTcPlan p;
+  p.sh = attention_tc_shape(B, Hq, Hkv, t->N, window_tc_lcap(Lcap, t->N, window, sinks));
+  WsCarver w;
+  const size_t rows = p.sh.P > 1 && !p.sh.fuse ? (size_t)B * Hkv * p.sh.P * t->N * (Hq / Hkv) : 0;
+  p.off_o = w.take<float>(rows * dh);
+  p.off_ml = w.take<float2>(rows);
+  p.total = w.total();
+  return p;
+}
+
+}  // namespace
+
 size_t attention_ext_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
                                int dtype, int window, int sinks, bool packed) {
   if (!packed && window <= 0) return attention_workspace(t, B, Hq, Hkv, dh, Lcap, dtype);
+  if (!packed && attention_tc_eligible(dtype, dh, Hq, Hkv))
+    return window_tc_plan(t, B, Hq, Hkv, dh, Lcap, window, sinks).total;
   return simt_plan(t, B, Hq, Hkv, dh, Lcap, window, sinks).total;
 }
 
 int attention_ext_launch(const AttnExtArgs& x, cudaStream_t st) {
-  if (!x.packed && x.window <= 0) return attention_launch(x.a, st);  // no window: the plain call
+  const AttnArgs& a = x.a;
+  if (!x.packed && a.window <= 0) return attention_launch(a, st);  // no window: the plain call
+  if (!x.packed && attention_tc_eligible(a.dtype, a.dh, a.Hq, a.Hkv)) {
+    const WindowTcPlan p =
+        window_tc_plan(a.tree, a.B, a.Hq, a.Hkv, a.dh, a.Lcap, a.window, a.sinks);
+    float* po = (float*)((uint8_t*)a.ws + p.off_o);
+    float2* pml = (float2*)((uint8_t*)a.ws + p.off_ml);
+    int rc = attention_tc_run(a, p.sh, po, pml, st);
+    if (rc || p.sh.P == 1 || p.sh.fuse) return rc;
+    return attention_combine_launch(a, po, pml, p.sh.P, st);
+  }
   return simt_launch(x, st);
 }
 

@@ -45,10 +45,18 @@
 // rank c merges rows [c R/P, (c+1) R/P) of the tile from all ranks through
 // distributed shared memory; or they write the partials to the workspace for
 // the combine kernel.
+//
+// With a sliding window (kWin) the prefix tiles of a sequence are those of
+// the sinks (from slot 0) and of the window (from the root's window start;
+// deeper nodes see up to K slots less, masked in the first window tile);
+// everything between is never read.  Work per step is then bounded by the
+// window: 64-node trees, 32 heads, 2048-token prefix, window 512: 6 key tiles
+// a CTA instead of 17.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "visible.cuh"
 
 namespace medusa {
 namespace cg = cooperative_groups;
@@ -84,16 +92,35 @@ struct TcAttnParams {
   __nv_bfloat16* out;
   float* po;
   float2* pml;
+  int window, sinks;  // kWin kernels
+  const int32_t* depth;
+  const int32_t* parent;
 };
 
 struct Range {
   int k_lo, k_hi, n_pre, n_tree;
+  // kWin: the chunk's first tile among the sink tiles (ns, slots [0, head))
+  // and the window tiles (from slot `tail`) after them
+  int t0, ns, head, tail;
 };
 
+template <bool kWin>
 __device__ __forceinline__ Range chunk_range(const TcAttnParams& p, int Lb, int chunk,
                                              bool seq_ok) {
-  Range rg{0, 0, 0, 0};
+  Range rg{0, 0, 0, 0, 0, 0, 0, 0};
   if (!seq_ok) return rg;
+  if constexpr (kWin) {
+    const VisibleRuns vr = visible_runs(Lb, p.N, p.window, p.sinks);
+    rg.head = vr.head;
+    rg.tail = vr.tail;
+    rg.ns = (vr.head + BN - 1) / BN;
+    const int nt = rg.ns + (Lb - vr.tail + BN - 1) / BN;
+    const int per = (nt + p.P - 1) / p.P;
+    rg.t0 = min(nt, chunk * per);
+    rg.n_pre = min(nt, rg.t0 + per) - rg.t0;
+    rg.n_tree = (chunk == p.P - 1) ? (p.N + BN - 1) / BN : 0;
+    return rg;
+  }
   int per = (Lb + p.P - 1) / p.P;
   per = (per + BN - 1) / BN * BN;  // whole 128-key tiles
   rg.k_lo = min(Lb, chunk * per);
@@ -135,24 +162,90 @@ __device__ __forceinline__ void write_row(const TcAttnParams& p, int b, int kvh,
   }
 }
 
+// First cache slot of key tile j (prefix tiles from the chunk start, then the
+// tree tiles from slot L_b).
+template <bool kWin>
+__device__ __forceinline__ int tile_key0(int j, int Lb, const Range& rg) {
+  if (j >= rg.n_pre) return Lb + (j - rg.n_pre) * BN;
+  if constexpr (kWin) {
+    const int g = rg.t0 + j;
+    return g < rg.ns ? g * BN : rg.tail + (g - rg.ns) * BN;
+  }
+  return rg.k_lo + j * BN;
+}
+
+// Keys of prefix tile j, from its first slot to the end of its run.
+template <bool kWin>
+__device__ __forceinline__ int tile_limit(int j, int Lb, const Range& rg) {
+  if constexpr (kWin) return (rg.t0 + j < rg.ns ? rg.head : Lb) - tile_key0<true>(j, Lb, rg);
+  return rg.k_hi - (rg.k_lo + j * BN);
+}
+
+// Rows of the staged tile j that hold slots some node sees or the caller has
+// written (< L_b + N); the V rows from there on are zeroed.  A sink tile ends
+// with the sinks: what follows may have been dropped from the cache.
+template <bool kWin>
+__device__ __forceinline__ int tile_rows(int j, int Lb, int N, const Range& rg) {
+  const int key0 = tile_key0<kWin>(j, Lb, rg);
+  if constexpr (kWin)
+    if (j < rg.n_pre && rg.t0 + j < rg.ns) return min(Lb + N - key0, rg.head - key0);
+  return Lb + N - key0;
+}
+
+// The query row's place in the window rule: its node's depth and that node.
+struct RowWin {
+  int depth, node;
+};
+
+// Prefix part of the masks below: keys past the run's end and, in the first
+// window tile, the slots before this row's own window (at most MEDUSA_MAX_K,
+// as the tile starts at the root's) that are no sinks.
+template <bool kWin>
+__device__ __forceinline__ void mask_prefix(float (&v)[64], int j, int hf, int Lb, const Range& rg,
+                                            const TcAttnParams& p, const RowWin& w) {
+  const int lim = tile_limit<kWin>(j, Lb, rg) - hf * 64;
+  if (lim < 64) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) v[c] = (c < lim) ? v[c] : -INFINITY;
+  }
+  if constexpr (kWin) {
+    if (hf == 0 && rg.t0 + j == rg.ns) {
+      const long long low = (long long)Lb + w.depth - p.window + 1 - rg.tail;
+#pragma unroll
+      for (int c = 0; c < MEDUSA_MAX_K; ++c)
+        if (c < low && rg.tail + c >= p.sinks) v[c] = -INFINITY;
+    }
+  }
+}
+
+// Ancestor word `wi` of a row without the ancestors outside its window
+// (windows of at most the tree's depth).
+__device__ __forceinline__ uint32_t window_anc_word(uint32_t word, int wi, int Lb,
+                                                    const TcAttnParams& p, const RowWin& w) {
+  int a = w.node;
+  for (int d = w.depth; a >= 0; --d) {
+    if (d <= w.depth - p.window && Lb + d >= p.sinks && (a >> 5) == wi) word &= ~(1u << (a & 31));
+    a = __ldg(p.parent + a);
+  }
+  return word;
+}
+
 // Scores of the 64-key half hf of 128-key tile j with masked columns set to
 // -inf: prefix keys past the chunk end, tree slots outside the row's
 // ancestor set (am = its ancestor bitmask words).
-__device__ __forceinline__ void mask_half(float (&v)[64], int j, int hf, const Range& rg, int N,
+template <bool kWin>
+__device__ __forceinline__ void mask_half(float (&v)[64], int j, int hf, int Lb, const Range& rg,
+                                          const TcAttnParams& p, const RowWin& w,
                                           const uint32_t (&am)[MEDUSA_MAX_N / 32]) {
   if (j < rg.n_pre) {
-    const int lim = rg.k_hi - (rg.k_lo + j * BN + hf * 64);
-    if (lim < 64) {
-#pragma unroll
-      for (int c = 0; c < 64; ++c) v[c] = (c < lim) ? v[c] : -INFINITY;
-    }
+    mask_prefix<kWin>(v, j, hf, Lb, rg, p, w);
   } else {
     // nodes 64q .. 64q+63, q < 4 as N <= 256; selects rather than a run-time
     // index keep am[] in registers
     const int q = 2 * (j - rg.n_pre) + hf;
     const uint32_t w0 = q == 0 ? am[0] : q == 1 ? am[2] : q == 2 ? am[4] : am[6];
     const uint32_t w1 = q == 0 ? am[1] : q == 1 ? am[3] : q == 2 ? am[5] : am[7];
-    const int nvalid = N - q * 64;
+    const int nvalid = p.N - q * 64;
 #pragma unroll
     for (int c = 0; c < 64; ++c) {
       const uint32_t word = c < 32 ? w0 : w1;
@@ -194,15 +287,14 @@ __device__ __forceinline__ float exp_pack64(const float (&v)[64], unsigned long 
 }
 
 // True when the 64-key half hf of key tile j has masked columns: a tree
-// tile, or the prefix tile that ends the chunk inside this half.
-__device__ __forceinline__ bool half_masked(int j, int hf, const Range& rg) {
-  return j >= rg.n_pre || rg.k_hi - (rg.k_lo + j * BN + hf * 64) < 64;
-}
-
-// First cache slot of key tile j (prefix tiles from the chunk start, then the
-// tree tiles from slot L_b).
-__device__ __forceinline__ int tile_key0(int j, int Lb, const Range& rg) {
-  return j < rg.n_pre ? rg.k_lo + j * BN : Lb + (j - rg.n_pre) * BN;
+// tile, the prefix tile that ends its run inside this half, or the first
+// window tile.
+template <bool kWin>
+__device__ __forceinline__ bool half_masked(int j, int hf, int Lb, const Range& rg) {
+  if (j >= rg.n_pre) return true;
+  if constexpr (kWin)
+    if (hf == 0 && rg.t0 + j == rg.ns) return true;
+  return tile_limit<kWin>(j, Lb, rg) - hf * 64 < 64;
 }
 
 // Zeroes rows [row0, BN) of a staged 128-key V tile (both 64-column halves;
@@ -287,6 +379,7 @@ __device__ __forceinline__ void cluster_merge(float* so, float2* sml, int qt, in
   cl.sync();  // every rank stays resident until the others have read its rows
 }
 
+template <bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmK,
@@ -338,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int Lb = p.L[b];
   const bool seq_ok = Lb >= 0 && (long long)Lb + p.N <= p.Lcap;
-  const Range rg = chunk_range(p, Lb, chunk, seq_ok);
+  const Range rg = chunk_range<kWin>(p, Lb, chunk, seq_ok);
   const int T = rg.n_pre + rg.n_tree;
 
   if (T == 0) {  // nothing to attend to in this chunk
@@ -406,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       for (int j = 0; j < T; ++j) {
         const int st = j % kStages;
-        const int key0 = j < rg.n_pre ? rg.k_lo + j * BN : Lb + (j - rg.n_pre) * BN;
+        const int key0 = tile_key0<kWin>(j, Lb, rg);
         dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
         const int z = b * p.Lcap + key0;
         if (!mbar_wait(&emp[st], ((uint32_t)(j / kStages) & 1u) ^ 1u, abort_flag)) break;
@@ -495,6 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t am[MEDUSA_MAX_N / 32];
 #pragma unroll
     for (int w = 0; w < MEDUSA_MAX_N / 32; ++w) am[w] = (w < p.W) ? p.anc[(size_t)node * p.W + w] : 0u;
+    RowWin rw{0, node};
+    if constexpr (kWin) {
+      rw.depth = __ldg(p.depth + node);
+      if (p.window <= rw.depth) {
+#pragma unroll
+        for (int w = 0; w < MEDUSA_MAX_N / 32; ++w) am[w] = window_anc_word(am[w], w, Lb, p, rw);
+      }
+    }
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const uint32_t tO = tmem + lane_base + 384u + (uint32_t)hf * 64u;  // this half's O columns
     const unsigned long long q2 = f2_pack(p.qscale, p.qscale);
@@ -511,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V rows of cache slots >= L_b + N in this tile (the tree tiles and the
       // prefix tile that ends the sequence): zeroed by the 256 softmax
       // threads once the tile has landed, before P(t) is released to P.V(t)
-      const int zrow = Lb + p.N - tile_key0(t, Lb, rg);
+      const int zrow = tile_rows<kWin>(t, Lb, p.N, rg);
       if (zrow < BN && !err) {
         const int vs = t % kStages;
         const bool vg = mbar_wait(&v_full[vs], (uint32_t)(t / kStages) & 1u, abort_flag);
@@ -531,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!err && warp_live) {
         tc_fence_after();
         tmem_ld64(tS, v);
-        mask_half(v, t, hf, rg, p.N, am);
+        mask_half<kWin>(v, t, hf, Lb, rg, p, rw, am);
         const uint32_t mine = bf16_bits_up(max64(v) * p.qscale);  // scale > 0
         tmax = __uint_as_float(mine << 16);
         xrow[hf * BM] = (uint16_t)mine;
@@ -581,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned long long m2 = f2_pack(-moff, -moff);
       uint32_t pk[32];
       // masked keys get exactly 0 (all-MUFU exponentials on masked halves)
-      l += half_masked(t, hf, rg) ? exp_pack64<true>(v, q2, m2, pk)
+      l += half_masked<kWin>(t, hf, Lb, rg) ? exp_pack64<true>(v, q2, m2, pk)
                                   : exp_pack64<false>(v, q2, m2, pk);
       tmem_st32(tS, pk);  // P over the S columns just read
       tc_fence_before();
@@ -675,19 +776,24 @@ static_assert(SMEM_PAIR <= 227 * 1024, "shared memory of the two-tile kernel");
 // mask_half with the ancestor words of the row's node read from memory (two
 // words, only for the tree tiles), so the kernel keeps no per-tile word sets
 // in registers.
-__device__ __forceinline__ void mask_half_mem(float (&v)[64], int j, int hf, const Range& rg,
-                                              int N, int W, const uint32_t* __restrict__ anc_row) {
+template <bool kWin>
+__device__ __forceinline__ void mask_half_mem(float (&v)[64], int j, int hf, int Lb,
+                                              const Range& rg, const TcAttnParams& p,
+                                              const RowWin& w,
+                                              const uint32_t* __restrict__ anc_row) {
   if (j < rg.n_pre) {
-    const int lim = rg.k_hi - (rg.k_lo + j * BN + hf * 64);
-    if (lim < 64) {
-#pragma unroll
-      for (int c = 0; c < 64; ++c) v[c] = (c < lim) ? v[c] : -INFINITY;
-    }
+    mask_prefix<kWin>(v, j, hf, Lb, rg, p, w);
   } else {
     const int q = 2 * (j - rg.n_pre) + hf;  // nodes 64q .. 64q+63
-    const uint32_t w0 = (2 * q < W) ? __ldg(anc_row + 2 * q) : 0u;
-    const uint32_t w1 = (2 * q + 1 < W) ? __ldg(anc_row + 2 * q + 1) : 0u;
-    const int nvalid = N - q * 64;
+    uint32_t w0 = (2 * q < p.W) ? __ldg(anc_row + 2 * q) : 0u;
+    uint32_t w1 = (2 * q + 1 < p.W) ? __ldg(anc_row + 2 * q + 1) : 0u;
+    if constexpr (kWin) {
+      if (p.window <= w.depth) {
+        w0 = window_anc_word(w0, 2 * q, Lb, p, w);
+        w1 = window_anc_word(w1, 2 * q + 1, Lb, p, w);
+      }
+    }
+    const int nvalid = p.N - q * 64;
 #pragma unroll
     for (int c = 0; c < 64; ++c) {
       const uint32_t word = c < 32 ? w0 : w1;
@@ -697,6 +803,7 @@ __device__ __forceinline__ void mask_half_mem(float (&v)[64], int j, int hf, con
   }
 }
 
+template <bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_tc_pair_kernel(const __grid_constant__ CUtensorMap tmQ,
                              const __grid_constant__ CUtensorMap tmK,
@@ -743,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int Lb = p.L[b];
   const bool seq_ok = Lb >= 0 && (long long)Lb + p.N <= p.Lcap;
-  const Range rg = chunk_range(p, Lb, chunk, seq_ok);
+  const Range rg = chunk_range<kWin>(p, Lb, chunk, seq_ok);
   const int T = rg.n_pre + rg.n_tree;
   const int qt0 = 2 * qpair;  // tile a; tile b = qt0 + 1
   const bool b_rows = (qt0 + 1) * BM < p.R;  // tile b has rows to write (uniform in a cluster)
@@ -823,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       for (int j = 0; j < T; ++j) {
         const int st = j % stages;
-        const int key0 = j < rg.n_pre ? rg.k_lo + j * BN : Lb + (j - rg.n_pre) * BN;
+        const int key0 = tile_key0<kWin>(j, Lb, rg);
         dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
         const int z = b * p.Lcap + key0;
         if (!mbar_wait(&emp[st], ((uint32_t)(j / stages) & 1u) ^ 1u, abort_flag)) break;
@@ -913,7 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grow = (qt0 + q) * BM + r;
     const bool row_ok = grow < p.R;
     const bool live = ((qt0 + q) * BM + q4 * 32) < p.R;  // warp-uniform
-    const uint32_t* anc_row = p.anc + (size_t)min(grow / p.G, p.N - 1) * p.W;
+    RowWin rw{0, min(grow / p.G, p.N - 1)};
+    if constexpr (kWin) rw.depth = __ldg(p.depth + rw.node);
+    const uint32_t* anc_row = p.anc + (size_t)rw.node * p.W;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     // Raises the running max to tmax when it grew by more than 2^kRescale:
@@ -968,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V rows of cache slots >= L_b + N in this tile: zeroed by tile a's
       // warpgroup before P_a(t) is released; the MMA thread issues P.V_b(t)
       // after P.V_a(t), so both products read the zeroed rows
-      const int zrow = Lb + p.N - tile_key0(t, Lb, rg);
+      const int zrow = tile_rows<kWin>(t, Lb, p.N, rg);
       if (q == 0 && zrow < BN) {
         const int vs = t % kPairVStages;
         const bool vg = mbar_wait(&v_full[vs], (uint32_t)(t / kPairVStages) & 1u, abort_flag);
@@ -985,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[64];
           tc_fence_after();
           tmem_ld64(tS + (uint32_t)(hf * 64), v);
-          mask_half_mem(v, t, hf, rg, p.N, p.W, anc_row);
+          mask_half_mem<kWin>(v, t, hf, Lb, rg, p, rw, anc_row);
           if (!maybe_rescale(max64(v) * p.qscale, t, hf == 1)) {
             ok = false;
             break;
@@ -996,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned long long m2 = f2_pack(-moff, -moff);
           uint32_t pk[32];
           // masked keys get exactly 0 (all-MUFU exponentials on masked halves)
-          l += half_masked(t, hf, rg) ? exp_pack64<true>(v, q2, m2, pk)
+          l += half_masked<kWin>(t, hf, Lb, rg) ? exp_pack64<true>(v, q2, m2, pk)
                                       : exp_pack64<false>(v, q2, m2, pk);
           tmem_st32(tS + (uint32_t)(hf * 64), pk);  // P over the S columns just read
         }
@@ -1060,8 +1169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-std::atomic<bool> g_smem_attr[64];  // per device: the kernel's shared-memory limit raised
-std::atomic<bool> g_smem_attr_pair[64];
+// per device: the kernels' shared-memory limit raised ([windowed][device])
+std::atomic<bool> g_smem_attr[2][64];
+std::atomic<bool> g_smem_attr_pair[2][64];
 
 // Clusters of P CTAs of the one-tile (pair = false) or two-tile kernel that
 // can be resident at once on the current device (0 when the query fails),
@@ -1075,11 +1185,12 @@ int max_active_clusters(bool pair, int P) {
   }
   const int v = cache[pair][dev][P].load(std::memory_order_relaxed);
   if (v) return v - 1;
-  const void* fn = pair ? (const void*)tree_attn_tc_pair_kernel : (const void*)tree_attn_tc_kernel;
+  const void* fn = pair ? (const void*)tree_attn_tc_pair_kernel<false>
+                        : (const void*)tree_attn_tc_kernel<false>;
   const size_t smem = pair ? SMEM_PAIR : SMEM;
-  if (pair ? ensure_max_smem(tree_attn_tc_pair_kernel, (int)SMEM_PAIR, g_smem_attr_pair,
+  if (pair ? ensure_max_smem(tree_attn_tc_pair_kernel<false>, (int)SMEM_PAIR, g_smem_attr_pair[0],
                              "cudaFuncSetAttribute(tree_attn_tc_pair_kernel)")
-           : ensure_max_smem(tree_attn_tc_kernel, (int)SMEM, g_smem_attr,
+           : ensure_max_smem(tree_attn_tc_kernel<false>, (int)SMEM, g_smem_attr[0],
                              "cudaFuncSetAttribute(tree_attn_tc_kernel)"))
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -1197,7 +1308,10 @@ int attention_tc_run(const AttnArgs& a, const TcShape& sh, float* po, float2* pm
     rc = make_tmap_bf16(&mV, a.v, 3, dims, strides, box);
     if (rc) return rc;
   }
-  int rc = ensure_max_smem(tree_attn_tc_kernel, (int)SMEM, g_smem_attr,
+  const bool win = a.window > 0;
+  auto* kern = win ? tree_attn_tc_kernel<true> : tree_attn_tc_kernel<false>;
+  auto* kern_pair = win ? tree_attn_tc_pair_kernel<true> : tree_attn_tc_pair_kernel<false>;
+  int rc = ensure_max_smem(kern, (int)SMEM, g_smem_attr[win],
                            "cudaFuncSetAttribute(tree_attn_tc_kernel)");
   if (rc) return rc;
   TcAttnParams p;
@@ -1218,11 +1332,15 @@ int attention_tc_run(const AttnArgs& a, const TcShape& sh, float* po, float2* pm
   p.out = (__nv_bfloat16*)a.out;
   p.po = po;
   p.pml = pml;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.depth = t->d_depth;
+  p.parent = t->d_parent;
   cudaError_t e;
   const bool pair = sh.tiles == 2;
   if (pair && P > 1 && !p.fuse) return fail(MEDUSA_ERR_UNSUPPORTED, "two-tile plan without merge");
   if (pair) {
-    rc = ensure_max_smem(tree_attn_tc_pair_kernel, (int)SMEM_PAIR, g_smem_attr_pair,
+    rc = ensure_max_smem(kern_pair, (int)SMEM_PAIR, g_smem_attr_pair[win],
                          "cudaFuncSetAttribute(tree_attn_tc_pair_kernel)");
     if (rc) return rc;
   }
@@ -1245,14 +1363,14 @@ int attention_tc_run(const AttnArgs& a, const TcShape& sh, float* po, float2* pm
     cfg.numAttrs = 2;
     if (pair) {
       cfg.dynamicSmemBytes = SMEM_PAIR;
-      e = cudaLaunchKernelEx(&cfg, tree_attn_tc_pair_kernel, mQ, mK, mV, p);
+      e = cudaLaunchKernelEx(&cfg, kern_pair, mQ, mK, mV, p);
     } else {
-      e = cudaLaunchKernelEx(&cfg, tree_attn_tc_kernel, mQ, mK, mV, p);
+      e = cudaLaunchKernelEx(&cfg, kern, mQ, mK, mV, p);
     }
   } else if (pair) {
-    e = launch_pdl(tree_attn_tc_pair_kernel, grid, dim3(kThreads), SMEM_PAIR, st, mQ, mK, mV, p);
+    e = launch_pdl(kern_pair, grid, dim3(kThreads), SMEM_PAIR, st, mQ, mK, mV, p);
   } else {
-    e = launch_pdl(tree_attn_tc_kernel, grid, dim3(kThreads), SMEM, st, mQ, mK, mV, p);
+    e = launch_pdl(kern, grid, dim3(kThreads), SMEM, st, mQ, mK, mV, p);
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "tree_attn_tc_kernel launch");

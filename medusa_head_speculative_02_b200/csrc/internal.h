@@ -132,6 +132,7 @@ struct AttnArgs {
   void* out;
   void* ws;
   size_t ws_bytes;
+  int window = 0, sinks = 0;  // sliding window (0: none) and sinks
 };
 size_t attention_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
                            int dtype);
@@ -187,10 +188,9 @@ int kv_compact_packed_launch(const PackedCache& c, int layers, int B, const int3
                              cudaStream_t st);
 
 // Tree attention over the 4-bit cache (packed != null; a.k and a.v unused)
-// and / or with a sliding window (window > 0).
+// and / or with a sliding window (a.window > 0).
 struct AttnExtArgs {
   AttnArgs a;
-  int window, sinks;
   const PackedCache* packed;
 };
 // Most slots a sequence's nodes can see.

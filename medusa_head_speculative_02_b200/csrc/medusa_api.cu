@@ -697,8 +697,9 @@ int attention_ext_call(const void* q, const void* k, const void* v, const Packed
       attention_ext_workspace(tree, B, Hq, Hkv, dh, Lcap, dtype, window, sinks, packed != nullptr);
   if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
     return fail(MEDUSA_ERR_INVALID_ARG, "workspace too small or not 16-byte aligned");
-  AttnExtArgs x{{q, k, v, prefix_len, tree, B, Hq, Hkv, dh, Lcap, scale, dtype, out, ws, ws_bytes},
-                window, sinks, packed};
+  AttnExtArgs x{{q, k, v, prefix_len, tree, B, Hq, Hkv, dh, Lcap, scale, dtype, out, ws, ws_bytes,
+                 window, sinks},
+                packed};
   return attention_ext_launch(x, (cudaStream_t)stream);
 }
 

@@ -100,19 +100,20 @@ def attention(q, k, v, Ls, plan, scale, window=0, sinks=0):
             continue
         vis = visible_fast(depth, anc, L, window, sinks).to(q.device)
         seen = vis.any(0)
-        for h in range(H):
-            kk = torch.where(seen[:, None], k[b, h, :L + N], 0.0)
-            vv = torch.where(seen[:, None], v[b, h, :L + N], 0.0)
-            for g in range(G):
-                qq = q[b, :, h * G + g].double()
-                s = (qq @ kk.T) * scale
-                s = s.masked_fill(~vis, -math.inf)
-                p = torch.softmax(s, -1)
-                out[b, :, h * G + g] = p @ vv
-                A[b, :, h * G + g] = p @ vv.abs()
-                sa = (qq.abs() @ kk.abs().T) * scale
-                S[b, :, h * G + g, 0] = sa.masked_fill(~vis, 0.0).amax(-1)
-                nv[b, :, h * G + g, 0] = vis.sum(-1) * vv.abs().max()
+        kk = torch.where(seen[:, None], k[b, :, :L + N], 0.0)[:, None]   # [H][1][keys][dh]
+        vv = torch.where(seen[:, None], v[b, :, :L + N], 0.0)[:, None]
+        qq = q[b].double().view(N, H, G, dh).permute(1, 2, 0, 3)          # [H][G][N][dh]
+        s = (qq @ kk.transpose(-1, -2)) * scale
+        p = torch.softmax(s.masked_fill(~vis, -math.inf), -1)
+        sa = ((qq.abs() @ kk.abs().transpose(-1, -2)) * scale).masked_fill(~vis, 0.0).amax(-1)
+
+        def put(dst, x):
+            dst[b].view(N, H, G, -1).copy_(x.permute(2, 0, 1, 3))
+        put(out, p @ vv)
+        put(A, p @ vv.abs())
+        put(S, sa[..., None])
+        put(nv, (vis.sum(-1)[None, None, :, None] * vv.abs().amax((-1, -2))[..., None, None])
+            .expand(H, G, N, 1).double())
     return out, A, S, nv
 
 
