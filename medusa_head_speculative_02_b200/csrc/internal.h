@@ -193,6 +193,11 @@ struct AttnExtArgs {
   AttnArgs a;
   const PackedCache* packed;
 };
+// 4-bit cache on the tcgen05 kernel (bf16, dh = 128; csrc/attention_packed_tc.cu)
+bool attention_packed_tc_eligible(int dtype, int dh);
+size_t attention_packed_tc_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap,
+                                     int window, int sinks);
+int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStream_t st);
 // Most slots a sequence's nodes can see.
 long long ext_max_keys(int Lcap, int N, int window, int sinks);
 size_t attention_ext_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
@@ -248,5 +253,10 @@ int sample_next_launch(const void* vlog, int dtype, const int32_t* alen, const i
 int make_tmap_bf16(void* map /* CUtensorMap* */, const void* base, int rank,
                    const uint64_t* dims, const uint64_t* strides_bytes,
                    const uint32_t* box);
+// Bytes with 64-byte swizzling (64-byte rows), and 32-bit words unswizzled.
+int make_tmap_u8_sw64(void* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box);
+int make_tmap_u32(void* map, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace medusa

@@ -81,8 +81,10 @@ int num_sms() {
   return 148;
 }
 
-int make_tmap_bf16(void* map, const void* base, int rank, const uint64_t* dims,
-                   const uint64_t* strides_bytes, const uint32_t* box) {
+namespace {
+int encode_tmap(void* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base,
+                int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                const uint32_t* box) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(MEDUSA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t gd[5], gs[4];
@@ -93,13 +95,29 @@ int make_tmap_bf16(void* map, const void* base, int rank, const uint64_t* dims,
     es[i] = 1;
   }
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides_bytes[i];
-  CUresult r = fn((CUtensorMap*)map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-                  const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  CUresult r = fn((CUtensorMap*)map, type, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(MEDUSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (code " + std::to_string((int)r) + ")");
   return MEDUSA_OK;
+}
+}  // namespace
+
+int make_tmap_bf16(void* map, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank,
+                     dims, strides_bytes, box);
+}
+int make_tmap_u8_sw64(void* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B, base, rank,
+                     dims, strides_bytes, box);
+}
+int make_tmap_u32(void* map, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, base, rank,
+                     dims, strides_bytes, box);
 }
 
 // ---------------------------------------------------------------- tree plan
