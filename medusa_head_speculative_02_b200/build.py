@@ -23,6 +23,9 @@ LIB = os.path.join(PKG, "libmedusa.so")
 LIB_DEBUG = os.path.join(PKG, "libmedusa_debug.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+# Compiled as a whole program: its kernel splits registers between warpgroups,
+# which the compiler ignores in relocatable device code.
+WHOLE_PROGRAM = {"attention_packed_tc.cu"}
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-Wall", "--expt-relaxed-constexpr", "-I", INCLUDE,
                      "-I", CSRC]
@@ -53,7 +56,8 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 
 def _compile(src: str, obj: str, extra: list[str]) -> None:
-    cmd = [nvcc()] + NVCC_FLAGS + extra + ["-c", src, "-o", obj]
+    flags = [f for f in NVCC_FLAGS if f != "-rdc=true" or os.path.basename(src) not in WHOLE_PROGRAM]
+    cmd = [nvcc()] + flags + extra + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")

@@ -23,7 +23,7 @@
 // Q's dims and of the output rows.  Unpacked K goes straight from registers to
 // TMEM, unpacked V to shared memory.
 //
-// A softmax thread owns one key and NC/2 query rows, so scores need no
+// A softmax thread owns one key and up to 64 query rows, so scores need no
 // cross-thread work in the common case: the running row maxima are kept in
 // shared memory and move only when a score exceeds its row's maximum by more
 // than 2^8 (one barrier vote of 128 threads per tile); the row sums stay in
@@ -31,12 +31,15 @@
 // scales, relative to a power of two >= the largest value scale seen times
 // 2^-7, are rounded once to fp16.  Statistics, sums and products are fp32.
 //
-// Warps: 0 TMA (codes and scales, a ring of tiles), 1 MMA issue, then the
-// unpack warps (4 for K and 4 for V, or 4 for both with 128 rows) and 8
-// softmax warps (2 per TMEM lane quadrant, NC/2 rows each).  TMEM: O^T, two
-// S^T buffers, two K buffers.
+// TMEM: O^T, two S^T buffers, two K buffers.
+// This source is compiled without relocatable device code: register splits
+// between warpgroups (setmaxnreg) are only honoured then, and without them the
+// softmax threads' 64 rows would spill.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
+#define MEDUSA_OWN_STATUS
 #include "common.cuh"
 #include "internal.h"
 #include "visible.cuh"
@@ -50,32 +53,46 @@ constexpr uint32_t kCodeTile = BK * DH / 2;   // 8 KB
 constexpr uint32_t kVTile = BK * DH * 2;      // 32 KB of fp16
 constexpr uint32_t kAtom = BK * 128;          // 128 rows of 128 bytes: 16 KB
 constexpr float kGrow = 8.0f;                 // log2 of the growth that moves a row maximum
-constexpr int kParStages = 8;
+constexpr uint32_t kStage = 2 * kCodeTile + 2 * BK * 4;  // K | V codes, K | V (scale, zero)
+constexpr int kScaleBufs = 4;
 
+// Warpgroups: 0 TMA and MMA issue, then unpack, then two of softmax.  Up to
+// 64 query rows the two softmax warpgroups take alternate key tiles, all rows
+// each, with their own maxima, sums and O^T (merged at the end): a tile's
+// chain of waits may then last two tiles.  128 rows are split in halves.
 template <int NC>
 struct Cfg {
-  static constexpr int UW = NC <= 64 ? 8 : 4;  // unpack warps
-  static constexpr int SW = 8;                 // softmax warps
-  static constexpr int kThreads = 32 * (2 + UW + SW);
-  static constexpr int CP = NC / 2;            // query rows per softmax thread
-  static constexpr int SB = CP < 32 ? CP : 32; // of them at a time
-  static constexpr int NSB = CP / SB;
+  static constexpr int kSets = NC <= 64 ? 2 : 1;
+  static constexpr int CP = kSets == 2 ? NC : NC / 2;  // query rows per softmax thread
+  static constexpr int BS = CP < 32 ? CP : 32;         // of them in one mask word
+  static constexpr int NB = CP / BS;
+  static constexpr int kState = 2 * CP;                // (softmax warpgroup, row) states
+  static constexpr int kUnpackWgs = NC <= 32 ? 2 : 1;  // K and V apart, or one for both
+  static constexpr int kThreads = 128 * (3 + kUnpackWgs);
+  // registers per thread after the split; their sum stays within the launch's
+  static constexpr int kRegs0 = NC <= 32 ? 64 : 56;
+  static constexpr int kRegsUnpack = NC <= 32 ? 72 : 80;
+  static constexpr int kRegsSoftmax = NC <= 32 ? 136 : 184;
+  static constexpr int kRegsLaunch = NC <= 32 ? 96 : 128;  // what 640 or 512 threads get
+  static_assert(kRegs0 + kUnpackWgs * kRegsUnpack + 2 * kRegsSoftmax <=
+                    (3 + kUnpackWgs) * kRegsLaunch, "register split");
   static constexpr int kStages = NC <= 64 ? 6 : 3;
   static constexpr uint32_t kQ = NC * DH * 2;
   static constexpr uint32_t kP = kAtom * ((NC + 63) / 64);
   static constexpr uint32_t oV = kQ;
   static constexpr uint32_t oP = oV + 2 * kVTile;
   static constexpr uint32_t oCode = oP + 2 * kP;
-  static constexpr uint32_t oPar = oCode + kStages * 2 * kCodeTile;
-  static constexpr uint32_t oMisc = oPar + kParStages * 2 * BK * 4;
-  static constexpr uint32_t kMisc = 512 + 4 * NC * 4 + NC * 8 + 4 * NC * 4 + 2 * 4 * 32 * 4 + 256;
+  static constexpr uint32_t oScale = oCode + kStages * kStage;
+  static constexpr uint32_t oMisc = oScale + kScaleBufs * 2 * BK * 4;
+  static constexpr uint32_t kMisc = 256 + 4 * kState * 4 + 3 * NC * 4 + 2 * 4 * CP * 4 +
+                                    2 * (4 * 4 + NB * 4 + 4) + (NC / BS) * (MEDUSA_MAX_K + 2) * 4;
   static constexpr size_t kSmem = 1024 + oMisc + kMisc;
-  static constexpr uint32_t kTmemCols = NC <= 32 ? 256 : 512;  // O | S S | K K
-  static constexpr uint32_t tS = NC;
-  static constexpr uint32_t tK = 3 * NC;
-  static_assert(3 * NC + 2 * 64 <= (int)kTmemCols, "TMEM columns");
+  static constexpr uint32_t kTmemCols = NC <= 32 ? 256 : 512;  // O (per set) | S S | K K
+  static constexpr uint32_t tS = kSets * NC;
+  static constexpr uint32_t tK = tS + 2 * NC;
+  static_assert(tK + 2 * 64 <= kTmemCols, "TMEM columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kQ % 1024 == 0 && oCode % 1024 == 0 && oPar % 128 == 0, "operand alignment");
+  static_assert(kQ % 1024 == 0 && oCode % 1024 == 0 && oScale % 128 == 0, "operand alignment");
 };
 
 struct PackedParams {
@@ -112,11 +129,36 @@ __device__ __forceinline__ void zero_pairs(uint32_t par, __half2& z24, __half2& 
   z20 = __float2half2_rn(-z * 0x1p-20f);
 }
 
+// Reduction over the lanes of a warp of N per-lane values each (N = 8, 16, 32),
+// transposed on the way: lane i returns value i mod N over all lanes.
+template <int N, typename Op>
+__device__ __forceinline__ float col_reduce(float (&a)[N], int lane, Op op) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float keep = up ? a[i + o] : a[i], send = up ? a[i] : a[i + o];
+      a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  float r = a[0];
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
+  return r;
+}
+
 template <int SB>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t t, float (&v)[SB]) {
   if constexpr (SB == 8) tmem_ld8(t, v);
   else if constexpr (SB == 16) tmem_ld16(t, v);
   else tmem_ld32(t, v);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Tiles of a sequence: the sinks' first, then from the root's window start.
@@ -145,51 +187,47 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   uint8_t* sQ = sm;
   uint8_t* sV = sm + C::oV;
   uint8_t* sP = sm + C::oP;
-  uint8_t* sCode = sm + C::oCode;                // [stage][K 8 KB | V 8 KB]
-  uint32_t* sPar = (uint32_t*)(sm + C::oPar);    // [stage][K 128 | V 128]
+  uint8_t* sCode = sm + C::oCode;                // [stage]
+  float* sScale = (float*)(sm + C::oScale);      // [4][K 128 | V 128]
   uint64_t* bars = (uint64_t*)(sm + C::oMisc);
   uint64_t* code_full = bars;                    // [kStages]
   uint64_t* code_empty = code_full + C::kStages; // [kStages]
-  uint64_t* par_full = code_empty + C::kStages;  // [kParStages]
-  uint64_t* par_empty = par_full + kParStages;   // [kParStages]
-  uint64_t* k_ready = par_empty + kParStages;    // [2] K unpacked in TMEM
-  uint64_t* v_ready = k_ready + 2;               // [2] V unpacked in smem
-  uint64_t* s_full = v_ready + 2;                // [2] S^T done (K buffer free)
-  uint64_t* s_free = s_full + 2;                 // [2] S^T read
-  uint64_t* p_full = s_free + 2;                 // [2] P^T written
-  uint64_t* pv_done = p_full + 2;                // [2] O^T updated (P and V buffers free)
+  uint64_t* k_ready = code_empty + C::kStages;   // [2] K unpacked in TMEM, scales in smem
+  uint64_t* pv_ready = k_ready + 2;              // [2] V unpacked and P^T written
+  uint64_t* s_full = pv_ready + 2;               // [2] S^T done (K buffer free)
+  uint64_t* s_free = s_full + 2;                 // [2] S^T and scales read
+  uint64_t* pv_done = s_free + 2;                // [2] O^T updated (P and V buffers free)
   uint64_t* mma_done = pv_done + 2;
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   unsigned* qmax = (unsigned*)(tmem_slot + 2);
-  static_assert((2 * 6 + 2 * kParStages + 13) * 8 + 16 <= 512, "barrier block");
-  float* nm = (float*)(sm + C::oMisc + 512);  // [NC] minus the row maximum (base 2)
-  float* fl = nm + NC;                        // [NC] rescale of the sums
-  float* fo = fl + NC;                        // [NC] rescale of O
-  float* lsum = fo + NC;                      // [NC]
-  int* cnode = (int*)(lsum + NC);             // [NC] node of the query row
+  static_assert((2 * 6 + 11) * 8 + 16 <= 256, "barrier block");
+  // per (softmax warpgroup, row)
+  float* nm = (float*)(sm + C::oMisc + 256);  // minus the row maximum (base 2)
+  float* fl = nm + C::kState;                 // rescale of the sums; at the end the row sum
+  float* fo = fl + C::kState;                 // rescale of O; at the end its factor
+  float* fd = fo + C::kState;                 // shift of the scores
+  int* cnode = (int*)(fd + C::kState);        // [NC] node of the query row
   int* cdepth = cnode + NC;                   // [NC]
-  float* lred = (float*)(cdepth + NC);        // [4][NC]
-  unsigned* red = (unsigned*)(lred + 4 * NC); // [2][4][32]
-  float* redv = (float*)(red + 2 * 4 * 32);   // [2][4]
+  int* crow = cdepth + NC;                    // [NC] node * Hq + query head, -1 past the last row
+  float* red = (float*)(crow + NC);           // [warpgroup][4][CP]
+  float* redv = red + 2 * 4 * C::CP;          // [warpgroup][4]
+  uint32_t* unset_s = (uint32_t*)(redv + 8);  // [warpgroup][NB] rows without a maximum yet
+  float* vref_s = (float*)(unset_s + 2 * C::NB);      // [warpgroup]
+  uint32_t* shallow = (uint32_t*)(vref_s + 2);        // [NC / BS][x]: rows of depth < x
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kWarps = C::kThreads / 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&code_full[i], 1);
-      mbar_init(&code_empty[i], C::UW);
-    }
-    for (int i = 0; i < kParStages; ++i) {
-      mbar_init(&par_full[i], 1);
-      mbar_init(&par_empty[i], C::UW + C::SW);
+      mbar_init(&code_empty[i], 4 * C::kUnpackWgs);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_ready[i], 4);
-      mbar_init(&v_ready[i], 4);
+      mbar_init(&pv_ready[i], 4 + 8 / C::kSets);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], C::SW);
-      mbar_init(&p_full[i], C::SW);
+      mbar_init(&s_free[i], 8 / C::kSets);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(mma_done, 1);
@@ -260,15 +298,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
   }
   for (int c = threadIdx.x; c < NC; c += C::kThreads) {
-    const int node = min((row0 + c) / p.G, p.N - 1);
+    const int r = row0 + c, node = min(r / p.G, p.N - 1);
     cnode[c] = node;
     cdepth[c] = p.depth[node];
-    nm[c] = 1e30f;  // no maximum yet
+    crow[c] = r < p.R ? node * p.Hq + kvh * p.G + (r - node * p.G) : -1;
   }
+  for (int c = threadIdx.x; c < C::kState; c += C::kThreads) nm[c] = 0.f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // warp-uniform
   griddep_launch_dependents();  // TMEM taken: the next kernel may be scheduled
   // 2^k brings the largest |q| into [2^13, 2^14)
   int kexp = 0;
@@ -287,26 +326,34 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         dst[2 * jj + h] = __float2half_rn(f[jj] * ((jj & 1) ? qs * 0.0625f : qs));
     }
   }
+  for (int e = threadIdx.x; e < (NC / C::BS) * (MEDUSA_MAX_K + 2); e += C::kThreads) {
+    const int g = e / (MEDUSA_MAX_K + 2), x = e - g * (MEDUSA_MAX_K + 2);
+    uint32_t m = 0u;
+    for (int c = 0; c < C::BS; ++c) m |= (uint32_t)(cdepth[g * C::BS + c] < x) << c;
+    shallow[e] = m;
+  }
   fence_proxy_async_smem();
   __syncthreads();
 
-  if (warp == 0) {
+  const int wg = warp >> 2, qd = warp & 3;
+  const int key = qd * 32 + lane;                          // this thread's key of a tile
+  const uint32_t lane_base = (uint32_t)(qd * 32) << 16;   // its TMEM lane quadrant
+  if (wg == 0) {
+    reg_dec<C::kRegs0>();
+    if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
       int issued = 0;
       for (int j = 0; j < T; ++j) {
-        const int st = j % C::kStages, ps = j % kParStages;
+        const int st = j % C::kStages;
         const int key0 = tl.tile(j0 + j) * BK;
         dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
         if (!mbar_wait(&code_empty[st], ((uint32_t)(j / C::kStages) & 1u) ^ 1u, abort_flag)) break;
-        if (!mbar_wait(&par_empty[ps], ((uint32_t)(j / kParStages) & 1u) ^ 1u, abort_flag)) break;
-        mbar_arrive_expect_tx(&par_full[ps], 2 * BK * 4);
-        tma_load_2d(sPar + ps * 2 * BK, &tmKp, &par_full[ps], key0, bk, pol);
-        tma_load_2d(sPar + ps * 2 * BK + BK, &tmVp, &par_full[ps], key0, bk, pol);
-        mbar_arrive_expect_tx(&code_full[st], 2 * kCodeTile);
-        uint8_t* dst = sCode + st * 2 * kCodeTile;
+        mbar_arrive_expect_tx(&code_full[st], kStage);
+        uint8_t* dst = sCode + st * kStage;
         tma_load_3d(dst, &tmKc, &code_full[st], 0, key0, bk, pol);
+        tma_load_2d(dst + 2 * kCodeTile, &tmKp, &code_full[st], key0, bk, pol);
+        tma_load_2d(dst + 2 * kCodeTile + BK * 4, &tmVp, &code_full[st], key0, bk, pol);
         tma_load_3d(dst + kCodeTile, &tmVc, &code_full[st], 0, key0, bk, pol);
         issued = j + 1;
       }
@@ -314,378 +361,405 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         // aborted: let the loads already issued land before the CTA exits
         for (int j = (issued > C::kStages ? issued - C::kStages : 0); j < issued; ++j)
           mbar_wait(&code_full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, nullptr);
-        for (int j = (issued > kParStages ? issued - kParStages : 0); j < issued; ++j)
-          mbar_wait(&par_full[j % kParStages], (uint32_t)(j / kParStages) & 1u, nullptr);
       }
     }
-  } else if (warp == 1) {
+    if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    // S(0), S(1), then PV(t), S(t + 2): S runs two tiles ahead
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = umma_idesc_f16_f32(BK, NC, false, false);
-      constexpr uint32_t idesc_o = umma_idesc_f16_f32(DH, NC, true, true);
-      const uint64_t dq = umma_desc_sw128_kmajor(smem_u32(sQ));
-      auto issue_s = [&](int t) -> bool {
-        const int bf = t & 1;
-        const uint32_t ph = (uint32_t)(t >> 1) & 1u;
-        if (!mbar_wait(&k_ready[bf], ph, abort_flag)) return false;
-        if (t >= 2 && !mbar_wait(&s_free[bf], ph ^ 1u, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t a = tmem + C::tK + (uint32_t)bf * 64u;
-        const uint32_t d = tmem + C::tS + (uint32_t)bf * NC;
+    // S(0), S(1), then S(t + 2) once S(t) has been read, and PV(t)
+    constexpr uint32_t idesc_s = umma_idesc_f16_f32(BK, NC, false, false);
+    constexpr uint32_t idesc_o = umma_idesc_f16_f32(DH, NC, true, true);
+    const uint64_t dq = umma_desc_sw128_kmajor(smem_u32(sQ));
+    const uint64_t dv0 = umma_desc_sw128(smem_u32(sV), kAtom, 1024u);
+    const uint64_t dp0 = umma_desc_sw128(smem_u32(sP), kAtom, 1024u);
+    auto issue_s = [&](int t) -> bool {
+      const int bf = t & 1;
+      const uint32_t ph = (uint32_t)(t >> 1) & 1u;
+      if (!mbar_wait_warp(&k_ready[bf], ph, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t a = tmem + C::tK + (uint32_t)bf * 64u;
+      const uint32_t d = tmem + C::tS + (uint32_t)bf * NC;
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          umma_bf16_ts(d, a + (uint32_t)kk * 8u,
-                       dq + (uint64_t)(((kk >> 2) * (NC * 128) + (kk & 3) * 32) >> 4), idesc_s,
-                       kk > 0 ? 1u : 0u);
-        umma_commit(&s_full[bf]);
-        return true;
-      };
-      auto issue_pv = [&](int t) -> bool {
-        const int bf = t & 1;
-        const uint32_t ph = (uint32_t)(t >> 1) & 1u;
-        if (!mbar_wait(&v_ready[bf], ph, abort_flag)) return false;
-        if (!mbar_wait(&p_full[bf], ph, abort_flag)) return false;
-        tc_fence_after();
-        const uint64_t dv = umma_desc_sw128(smem_u32(sV + bf * kVTile), kAtom, 1024u);
-        const uint64_t dp = umma_desc_sw128(smem_u32(sP + bf * C::kP), kAtom, 1024u);
+      for (int kk = 0; kk < DH / 16; ++kk)
+        umma_f16_ts_warp(d, a + (uint32_t)kk * 8u,
+                         dq + (uint64_t)(((kk >> 2) * (NC * 128) + (kk & 3) * 32) >> 4), idesc_s,
+                         kk > 0 ? 1u : 0u);
+      umma_commit_warp(&s_full[bf]);
+      return true;
+    };
+    auto issue_pv = [&](int t) -> bool {
+      const int bf = t & 1;
+      const uint32_t ph = (uint32_t)(t >> 1) & 1u;
+      if (!mbar_wait_warp(&pv_ready[bf], ph, abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t dv = dv0 + (uint64_t)(bf * (kVTile >> 4));
+      const uint64_t dp = dp0 + (uint64_t)(bf * (C::kP >> 4));
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          umma_bf16(tmem, dv + (uint64_t)((kk * 16 * 128) >> 4), dp + (uint64_t)((kk * 16 * 128) >> 4),
-                    idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&pv_done[bf]);
-        return true;
-      };
-      bool ok = true;
-      for (int t = 0; t < 2 && t < T && ok; ++t) ok = issue_s(t);
-      for (int t = 0; t < T && ok; ++t) {
-        ok = issue_pv(t);
-        if (ok && t + 2 < T) ok = issue_s(t + 2);
-      }
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0u, nullptr);
-    }
-  } else if (warp < 2 + C::UW) {
-    // ---------------------------------------------------------------- unpack
-    const bool doK = C::UW == 4 || warp < 6, doV = C::UW == 4 || warp >= 6;
-    const int qd = warp & 3;
-    const int key = qd * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    const int sw = (key >> 1) & 3;  // 64-byte swizzle of the code rows
+      for (int kk = 0; kk < BK / 16; ++kk)
+        umma_f16_warp(tmem + (uint32_t)((t & (C::kSets - 1)) * NC), dv + (uint64_t)((kk * 16 * 128) >> 4),
+                      dp + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
+                      (t >= C::kSets || kk > 0) ? 1u : 0u);
+      umma_commit_warp(&pv_done[bf]);
+      return true;
+    };
     bool ok = true;
+    for (int t = 0; t < 2 && t < T && ok; ++t) ok = issue_s(t);
     for (int t = 0; t < T && ok; ++t) {
-      const int st = t % C::kStages, ps = t % kParStages, bf = t & 1;
+      if (t + 2 < T)
+        ok = mbar_wait_warp(&s_free[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag) && issue_s(t + 2);
+      ok = ok && issue_pv(t);
+    }
+    umma_commit_warp(mma_done);
+    mbar_wait(mma_done, 0u, nullptr);
+    }
+  } else if (wg <= C::kUnpackWgs) {
+    // ---------------------------------------------------------------- unpack
+    reg_dec<C::kRegsUnpack>();
+    const bool doK = wg == 1, doV = wg == C::kUnpackWgs;
+    const int sw = (key >> 1) & 3;  // 64-byte swizzle of the code rows
+    // cscale: scores are acc * 2^24 / 2^k * scale * log2(e) * sk
+    const float cscale = p.scale2 * ldexpf(1.f, 24 - kexp);
+    for (int t = 0; t < T; ++t) {
+      const int st = t % C::kStages, bf = t & 1;
       const uint32_t prev = ((uint32_t)(t >> 1) & 1u) ^ 1u;
-      bool good = mbar_wait(&par_full[ps], (uint32_t)(t / kParStages) & 1u, abort_flag) &&
-                  mbar_wait(&code_full[st], (uint32_t)(t / C::kStages) & 1u, abort_flag);
-      if (!__all_sync(0xffffffffu, good)) break;
-      uint32_t kw[16], vw[16], kp = 0u, vp = 0u;
-      const uint8_t* row = sCode + st * 2 * kCodeTile + key * 64;
+      if (!mbar_wait_warp(&code_full[st], (uint32_t)(t / C::kStages) & 1u, abort_flag)) break;
+      const uint8_t* row = sCode + st * kStage + key * 64;
+      const uint32_t* par = (const uint32_t*)(sCode + st * kStage + 2 * kCodeTile);
+      const uint32_t kp = par[key], vp = par[BK + key];
+      uint32_t w[16];
+      __half2 z24, z20;
       if (doK) {
-        kp = sPar[ps * 2 * BK + key];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(&kw[4 * i]) = *reinterpret_cast<const uint4*>(row + ((i ^ sw) << 4));
-      }
-      if (doV) {
-        vp = sPar[ps * 2 * BK + BK + key];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(&vw[4 * i]) =
-              *reinterpret_cast<const uint4*>(row + kCodeTile + ((i ^ sw) << 4));
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&par_empty[ps]);
-        mbar_arrive(&code_empty[st]);
-      }
-      if (doK) {
-        if (t >= 2) {  // S(t - 2) has read this K buffer
-          good = mbar_wait(&s_full[bf], prev, abort_flag);
-          if (!__all_sync(0xffffffffu, good)) break;
+          *reinterpret_cast<uint4*>(&w[4 * i]) = *reinterpret_cast<const uint4*>(row + ((i ^ sw) << 4));
+        if (!doV) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&code_empty[st]);
         }
+        if (t >= 2) {  // S(t - 2) has read this K buffer
+          if (!mbar_wait_warp(&s_full[bf], prev, abort_flag)) break;
+        }
+        // softmax(t - 4) has read this scale buffer: S(t - 2) was issued after s_free(t - 4)
+        sScale[(t & (kScaleBufs - 1)) * 2 * BK + key] = bf16_lo(kp) * cscale;
+        sScale[(t & (kScaleBufs - 1)) * 2 * BK + BK + key] = bf16_lo(vp);
         tc_fence_after();
-        __half2 z24, z20;
         zero_pairs(kp, z24, z20);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t r[32];
+        for (int hh = 0; hh < 4; ++hh) {
+          uint32_t r[16];
 #pragma unroll
-          for (int w = 0; w < 8; ++w) unpack_word(kw[hh * 8 + w], z24, z20, r + 4 * w);
-          tmem_st32(tmem + lane_base + C::tK + (uint32_t)(bf * 64 + hh * 32), r);
+          for (int i = 0; i < 4; ++i) unpack_word(w[hh * 4 + i], z24, z20, r + 4 * i);
+          tmem_st16_nowait(tmem + lane_base + C::tK + (uint32_t)(bf * 64 + hh * 16), r);
         }
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_ready[bf]);
       }
       if (doV) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(&w[4 * i]) =
+              *reinterpret_cast<const uint4*>(row + kCodeTile + ((i ^ sw) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&code_empty[st]);
         if (t >= 2) {  // PV(t - 2) has read this V buffer
-          good = mbar_wait(&pv_done[bf], prev, abort_flag);
-          if (!__all_sync(0xffffffffu, good)) break;
+          if (!mbar_wait_warp(&pv_done[bf], prev, abort_flag)) break;
         }
-        __half2 z24, z20;
         zero_pairs(vp, z24, z20);
         uint8_t* dst = sV + bf * kVTile + key * 128;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
+        for (int i = 0; i < 16; ++i) {
           uint32_t r[4];
-          unpack_word(vw[w], z24, z20, r);
-          *reinterpret_cast<uint4*>(dst + (w >> 3) * kAtom + (((w & 7) ^ (key & 7)) << 4)) =
+          unpack_word(w[i], z24, z20, r);
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * kAtom + (((i & 7) ^ (key & 7)) << 4)) =
               make_uint4(r[0], r[1], r[2], r[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ready[bf]);
+        if (lane == 0) mbar_arrive(&pv_ready[bf]);
       }
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const int hf = (warp - (2 + C::UW)) >> 2;  // query rows [hf CP, hf CP + CP)
-    const int qd = warp & 3;
-    const int key = qd * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    const int gt = (int)threadIdx.x - 32 * (2 + C::UW + 4 * hf);  // thread of the group
-    // scores: acc * 2^24 / 2^k * scale * log2(e) * sk
-    const float cscale = p.scale2 * ldexpf(1.f, 24 - kexp);
-    unsigned long long lacc[C::CP / 2];
+    reg_inc<C::kRegsSoftmax>();
+    const int g = wg - 1 - C::kUnpackWgs;       // softmax warpgroup
+    const int bar_id = 1 + g;
+    const int st0 = g * C::CP;                   // its row states
+    const int col0 = C::kSets == 2 ? 0 : st0;    // its query rows
+    const uint32_t tO = tmem + lane_base + (uint32_t)st0;  // (sets: its own O^T)
+    float lacc[C::CP];
 #pragma unroll
-    for (int c = 0; c < C::CP / 2; ++c) lacc[c] = 0ull;
-    float vref[C::NSB];
+    for (int c = 0; c < C::CP; ++c) lacc[c] = 0.f;
+    float vref = 0x1p-120f;
+    constexpr uint32_t kAll = 0xffffffffu >> (32 - C::BS);
+    uint32_t unset[C::NB];  // rows that have seen no key: their maximum is still open
 #pragma unroll
-    for (int s = 0; s < C::NSB; ++s) vref[s] = 0x1p-120f;
+    for (int n = 0; n < C::NB; ++n) unset[n] = kAll;
+    // tiles with tree or unused slots (from m_hi), or slots outside some row's window (to m_lo)
+    const int m_hi = Lb / BK;
+    const long long wl = (long long)Lb + p.K - p.window;
+    const int m_lo = p.window > 0 && wl >= 0 ? (int)(wl / BK) : -1;
     bool ok = true, err = false;
-    for (int t = 0; t < T && ok; ++t) {
-      const int bf = t & 1, ps = t % kParStages;
+    for (int t = C::kSets == 2 ? g : 0; t < T; t += C::kSets) {
+      const int bf = t & 1;
       const uint32_t ph = (uint32_t)(t >> 1) & 1u;
       const int tile = tl.tile(j0 + t);
-      bool good = mbar_wait(&par_full[ps], (uint32_t)(t / kParStages) & 1u, abort_flag);
-      const uint32_t kp = sPar[ps * 2 * BK + key], vp = sPar[ps * 2 * BK + BK + key];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&par_empty[ps]);
-      good = good && mbar_wait(&s_full[bf], ph, abort_flag);
-      // the P buffer: PV(t - 2) has read it
-      if (t >= 2) good = good && mbar_wait(&pv_done[bf], ph ^ 1u, abort_flag);
-      err = err || !__all_sync(0xffffffffu, good);
+      err = err || !mbar_wait_warp(&s_full[bf], ph, abort_flag);
       tc_fence_after();
-      const float ks = bf16_lo(kp) * cscale;
-      const unsigned long long ks2 = f2_pack(ks, ks);
-      const int slot = tile * BK + key;
-      // tiles with a tree or unused slot, or one that is not in every row's window
-      const bool masked = (long long)(tile + 1) * BK > Lb ||
-                          (p.window > 0 && (long long)tile * BK <= (long long)Lb + p.K - p.window);
+      const float ks = sScale[(t & (kScaleBufs - 1)) * 2 * BK + key];
+      float sv = sScale[(t & (kScaleBufs - 1)) * 2 * BK + BK + key];
+      // scores relative to the row maxima, base 2
+      float y[C::CP];
+      if constexpr (C::CP == 64) tmem_ld64(tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0), y);
+      else tmem_ld_cols<C::CP>(tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0), y);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[bf]);
+      const bool masked = tile >= m_hi || tile <= m_lo;
+      uint32_t vm[C::NB];  // rows that see this key
 #pragma unroll
-      for (int s = 0; s < C::NSB; ++s) {
-        const int col0 = hf * C::CP + s * C::SB;
-        uint32_t vm = 0xffffffffu;  // rows that see this key
-        if (masked) {
-          vm = 0u;
-          if (slot < Lb + p.N) {
-            const int a = slot - Lb;
-            const int pos = a < 0 ? slot : Lb + __ldg(p.depth + a);
-            for (int c = 0; c < C::SB; ++c) {
-              bool vis = in_window(pos, Lb + cdepth[col0 + c], p.window, p.sinks);
-              if (a >= 0)
-                vis = vis && ((__ldg(p.anc + (size_t)cnode[col0 + c] * p.W + (a >> 5)) >> (a & 31)) & 1u);
-              vm |= (uint32_t)vis << c;
+      for (int n = 0; n < C::NB; ++n) vm[n] = kAll;
+      if (masked) {
+        const int a0 = tile * BK + qd * 32 - Lb;  // tree node of lane 0 (negative: a prefix slot)
+        const int a = a0 + lane;
+        uint32_t any = 0u;
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) {
+          if (a0 > -32) {
+            // lane c: row c's ancestor bits of this warp's 32 keys, then transposed
+            uint32_t w = 0u;
+            if (lane < C::BS) {
+              const uint32_t* ar = p.anc + (size_t)cnode[col0 + n * C::BS + lane] * p.W;
+              const int wi = a0 >> 5;  // -1: prefix slots first
+              const uint32_t w0 = wi >= 0 && wi < p.W ? __ldg(ar + wi) : 0u;
+              const uint32_t w1 = wi + 1 < p.W ? __ldg(ar + wi + 1) : 0u;
+              w = __funnelshift_r(w0, w1, a0 & 31);
             }
+            uint32_t tm = 0u;
+#pragma unroll
+            for (int c = 0; c < C::BS; ++c)
+              tm |= ((__shfl_sync(0xffffffffu, w, c) >> lane) & 1u) << c;
+            if (a >= 0) vm[n] = a < p.N ? tm : 0u;
+          }
+          if (p.window > 0 && a < p.N) {
+            const int dp = a < 0 ? a : __ldg(p.depth + a);  // position - L_b
+            if (Lb + dp >= p.sinks)
+              vm[n] &= shallow[(col0 / C::BS + n) * (MEDUSA_MAX_K + 2) +
+                               (int)min((long long)MEDUSA_MAX_K + 1, max(0ll, (long long)dp + p.window))];
+          }
+          any |= vm[n];
+        }
+        if (any == 0u) sv = 0.f;
+      }
+      const float4* nm4 = reinterpret_cast<const float4*>(nm + st0);
+#pragma unroll
+      for (int c = 0; c < C::CP / 4; ++c) {
+        const float4 n = nm4[c];
+        y[4 * c] = fmaf(y[4 * c], ks, n.x);
+        y[4 * c + 1] = fmaf(y[4 * c + 1], ks, n.y);
+        y[4 * c + 2] = fmaf(y[4 * c + 2], ks, n.z);
+        y[4 * c + 3] = fmaf(y[4 * c + 3], ks, n.w);
+      }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < C::CP; ++c) y[c] = (vm[c / C::BS] >> (c % C::BS)) & 1u ? y[c] : -INFINITY;
+      }
+      float ym[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < C::CP / 2; ++c) ym[c & 3] = max3(ym[c & 3], y[2 * c], y[2 * c + 1]);
+      uint32_t fresh = 0u;
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) fresh |= vm[n] & unset[n];
+      if (bar_red_or(bar_id, 128,
+                     err || max3(ym[0], ym[1], fmaxf(ym[2], ym[3])) > kGrow || fabsf(sv) > vref ||
+                         fresh != 0u)) {
+        // a row maximum or the value scale grew (or a row met its first key):
+        // move them for the whole warpgroup, rescale the sums and O
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) {
+          float a[C::BS];
+#pragma unroll
+          for (int c = 0; c < C::BS; ++c) a[c] = y[n * C::BS + c];
+          const float m = col_reduce<C::BS>(a, lane, [](float x, float z) { return fmaxf(x, z); });
+          if (lane < C::BS) red[(g * 4 + qd) * C::CP + n * C::BS + lane] = m;
+        }
+        const uint32_t av = __float_as_uint(fabsf(sv));
+        const unsigned sb = __reduce_max_sync(0xffffffffu, av < 0x7f800000u ? av : 0u);
+        if (lane == 0) redv[g * 4 + qd] = __uint_as_float(sb);
+        if (bar_red_or(bar_id, 128, err)) {
+          ok = false;
+          break;
+        }
+        // power of two >= the largest scale, kept in [2^-120, 2^119]
+        const float* rv = redv + g * 4;
+        const uint32_t bb = __float_as_uint(fmaxf(fmaxf(rv[0], rv[1]), fmaxf(rv[2], rv[3])));
+        const int ex = min(246, max(7, (int)((bb >> 23) + ((bb & 0x7fffffu) ? 1 : 0))));
+        const float nref = fmaxf(vref, __uint_as_float((uint32_t)ex << 23));
+        const float fv = vref / nref;
+        vref = nref;
+        if (qd == 0) {  // the warpgroup's first warp: lane c is row c of each block
+#pragma unroll
+          for (int n = 0; n < C::NB; ++n) {
+            const bool mine = lane < C::BS;
+            const int c = n * C::BS + (mine ? lane : 0);
+            const float* rr = red + g * 4 * C::CP + c;
+            const float x = fmaxf(fmaxf(rr[0], rr[C::CP]), fmaxf(rr[2 * C::CP], rr[3 * C::CP]));
+            const bool open = (unset[n] >> lane) & 1u;
+            const bool seen = mine && x != -INFINITY;
+            float d = 0.f, f = 1.f;  // shift of the maximum, factor of the sums
+            if (seen && (open || x > kGrow)) {
+              d = -x;
+              f = open ? 0.f : exp2f(-x);
+            }
+            if (mine) {
+              nm[st0 + c] += d;
+              fd[st0 + c] = d;
+              fl[st0 + c] = f;
+              fo[st0 + c] = f * fv;
+            }
+            const unsigned sn = __ballot_sync(0xffffffffu, seen);
+            if (lane == 0) unset_s[g * C::NB + n] = unset[n] & ~sn;
           }
         }
-        const uint32_t ts = tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0);
-        const float sv = vm != 0u ? bf16_lo(vp) : 0.f;
-        unsigned long long y[C::SB / 2];
-        const ulonglong2* nm2 = reinterpret_cast<const ulonglong2*>(nm + col0);
-        float ymax = -INFINITY;
-        auto scores = [&]() {  // relative to the row maxima, base 2
-          constexpr int LD = C::SB < 16 ? C::SB : 16;
+        named_bar_sync(bar_id, 128);
 #pragma unroll
-          for (int c0 = 0; c0 < C::SB; c0 += LD) {
-            float v[LD];
-            tmem_ld_cols<LD>(ts + (uint32_t)c0, v);
+        for (int n = 0; n < C::NB; ++n) unset[n] = unset_s[g * C::NB + n];
 #pragma unroll
-            for (int c = 0; c < LD / 4; ++c) {
-              const ulonglong2 n2 = nm2[c0 / 4 + c];
-              y[c0 / 2 + 2 * c] = f2_fma(f2_pack(v[4 * c], v[4 * c + 1]), ks2, n2.x);
-              y[c0 / 2 + 2 * c + 1] = f2_fma(f2_pack(v[4 * c + 2], v[4 * c + 3]), ks2, n2.y);
-            }
-          }
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < C::SB / 2; ++c) {
-              float a, d;
-              f2_unpack(y[c], a, d);
-              a = (vm >> (2 * c)) & 1u ? a : -INFINITY;
-              d = (vm >> (2 * c + 1)) & 1u ? d : -INFINITY;
-              y[c] = f2_pack(a, d);
-            }
-          }
-        };
-        scores();
-#pragma unroll
-        for (int c = 0; c < C::SB / 2; ++c) {
-          float a, d;
-          f2_unpack(y[c], a, d);
-          ymax = fmaxf(ymax, fmaxf(a, d));
+        for (int c = 0; c < C::CP; ++c) {
+          lacc[c] *= fl[st0 + c];
+          y[c] += fd[st0 + c];
         }
-        if (bar_red_or(1 + hf, 128, err || ymax > kGrow || fabsf(sv) > vref[s])) {
-          // a row maximum or the value scale grew: move both for the whole
-          // group, rescale the sums and O
+        if (t >= C::kSets) {  // O holds the PV of this warpgroup's earlier tiles
+          const int tp = t - C::kSets;
+          if (mbar_wait_warp(&pv_done[tp & 1], (uint32_t)(tp >> 1) & 1u, abort_flag)) {
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < C::SB; ++c) {
-            float x = tmem_ld1(ts + (uint32_t)c);
-            x = (vm >> c) & 1u ? x * ks : -INFINITY;
-            const unsigned o = __reduce_max_sync(0xffffffffu, f32_order(x));
-            if (lane == 0) red[(hf * 4 + qd) * 32 + c] = o;
-          }
-          const unsigned sb = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sv)) < 0x7f800000u
-                                                                  ? __float_as_uint(fabsf(sv))
-                                                                  : 0u);
-          if (lane == 0) redv[hf * 4 + qd] = __uint_as_float(sb);
-          if (bar_red_or(1 + hf, 128, err)) {
-            ok = false;
-            break;
-          }
-          // power of two >= the largest scale, kept in [2^-120, 2^119]
-          const float big = fmaxf(fmaxf(redv[hf * 4], redv[hf * 4 + 1]),
-                                  fmaxf(redv[hf * 4 + 2], redv[hf * 4 + 3]));
-          const uint32_t bb = __float_as_uint(big);
-          const int ex = min(246, max(7, (int)((bb >> 23) + ((bb & 0x7fffffu) ? 1 : 0))));
-          const float nref = fmaxf(vref[s], __uint_as_float((uint32_t)ex << 23));
-          const float fv = vref[s] / nref;
-          vref[s] = nref;
-          if (gt < C::SB) {
-            const unsigned* rr = red + hf * 128 + gt;
-            const float x = order_f32(max(max(rr[0], rr[32]), max(rr[64], rr[96])));
-            const float old = nm[col0 + gt];
-            float f = 1.f;
-            if (x != -INFINITY && (old == 1e30f || !(x + old <= kGrow))) {
-              f = old == 1e30f ? 0.f : exp2f(-old - x);
-              nm[col0 + gt] = -x;
+            for (int c0 = 0; c0 < C::CP; c0 += 8) {
+              float o8[8];
+              tmem_ld8(tO + (uint32_t)c0, o8);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o8[e] *= fo[st0 + c0 + e];
+              tmem_st8(tO + (uint32_t)c0, o8);
             }
-            fl[col0 + gt] = f;
-            fo[col0 + gt] = f * fv;
+          } else {
+            err = true;  // reported at the next vote
           }
-          named_bar_sync(1 + hf, 128);
-#pragma unroll
-          for (int c = 0; c < C::SB / 2; ++c)
-            lacc[s * (C::SB / 2) + c] =
-                f2_mul(lacc[s * (C::SB / 2) + c],
-                       *reinterpret_cast<const unsigned long long*>(fl + col0 + 2 * c));
-          if (t > 0) {  // O holds PV(0 .. t - 1)
-            const bool w_ok = mbar_wait(&pv_done[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u, abort_flag);
-            if (__all_sync(0xffffffffu, w_ok)) {
-              tc_fence_after();
-#pragma unroll 1
-              for (int c0 = 0; c0 < C::SB; c0 += 8) {
-                float o8[8];
-                const uint32_t ta = tmem + lane_base + (uint32_t)(col0 + c0);
-                tmem_ld8(ta, o8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o8[e] *= fo[col0 + c0 + e];
-                tmem_st8(ta, o8);
-              }
-            } else {
-              err = true;  // reported at the next vote
-            }
-          }
-          scores();
         }
-        if (s == C::NSB - 1) {  // S^T read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[bf]);
-        }
-        // weights, and weights x value scales as fp16 in this key's row of P^T
-        const float vn = sv * __uint_as_float((261u << 23) - __float_as_uint(vref[s]));
-        const unsigned long long vn2 = f2_pack(vn, vn);
-        uint8_t* prow = sP + bf * C::kP + (col0 >> 6) * kAtom + key * 128;
+      }
+      // PV(t - 2) has read this P buffer
+      if (t >= 2) err = err || !mbar_wait_warp(&pv_done[bf], ph ^ 1u, abort_flag);
+      // weights, and weights x value scales as fp16 in this key's row of P^T
+      const float vn = sv * __uint_as_float((261u << 23) - __float_as_uint(vref));
+      uint8_t* prow = sP + bf * C::kP + (col0 >> 6) * kAtom + key * 128;
+      auto weights = [&](auto is_masked) {
 #pragma unroll
-        for (int c8 = 0; c8 < C::SB / 8; ++c8) {
+        for (int c8 = 0; c8 < C::CP / 8; ++c8) {
           uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int c = c8 * 4 + e;
-            float a, d;
-            f2_unpack(y[c], a, d);
-            const unsigned long long w2 = f2_pack(ex2_approx(a), ex2_approx(d));
-            lacc[s * (C::SB / 2) + c] = f2_add(lacc[s * (C::SB / 2) + c], w2);
-            f2_unpack(f2_mul(w2, vn2), a, d);
-            if (masked) {  // 0, not 0 * NaN, for rows that do not see the key
-              a = (vm >> (2 * c)) & 1u ? a : 0.f;
-              d = (vm >> (2 * c + 1)) & 1u ? d : 0.f;
+            const int c = c8 * 8 + 2 * e;
+            float a = ex2_approx(y[c]), d = ex2_approx(y[c + 1]);
+            lacc[c] += a;
+            lacc[c + 1] += d;
+            a *= vn;
+            d *= vn;
+            if constexpr (decltype(is_masked)::value) {
+              // 0, not 0 * NaN, for rows that do not see the key
+              a = (vm[c / C::BS] >> (c % C::BS)) & 1u ? a : 0.f;
+              d = (vm[c / C::BS] >> (c % C::BS + 1)) & 1u ? d : 0.f;
             }
             const __half2 hh = __floats2half2_rn(a, d);
             h[e] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          *reinterpret_cast<uint4*>(prow + (((((col0 & 63) >> 3) + c8) ^ (key & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(prow + ((c8 ^ (key & 7)) << 4)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
-      }
-      if (!ok) break;
+      };
+      if (masked) weights(std::true_type{});
+      else weights(std::false_type{});
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[bf]);
+      if (lane == 0) mbar_arrive(&pv_ready[bf]);
     }
     ok = ok && !err;
-    if (ok) {
+    if (ok) {  // the last PV: every earlier one is done too
       const bool good = mbar_wait(&pv_done[(T - 1) & 1], (uint32_t)((T - 1) >> 1) & 1u, abort_flag);
       ok = __all_sync(0xffffffffu, good);
     }
-    // row sums over the 128 keys
+    // row sums over the keys of this warpgroup
 #pragma unroll
-    for (int c = 0; c < C::CP / 2; ++c) {
-      float a, d;
-      f2_unpack(lacc[c], a, d);
+    for (int n = 0; n < C::NB; ++n) {
+      float a[C::BS];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        d += __shfl_xor_sync(0xffffffffu, d, o);
-      }
-      if (lane == 0) {
-        lred[qd * NC + hf * C::CP + 2 * c] = a;
-        lred[qd * NC + hf * C::CP + 2 * c + 1] = d;
-      }
+      for (int c = 0; c < C::BS; ++c) a[c] = lacc[n * C::BS + c];
+      const float ls = col_reduce<C::BS>(a, lane, [](float x, float z) { return x + z; });
+      if (lane < C::BS) red[(g * 4 + qd) * C::CP + n * C::BS + lane] = ls;
     }
-    const bool bad = bar_red_or(1 + hf, 128, !ok);
-    if (gt < C::CP) {
-      const int c = hf * C::CP + gt;
-      lsum[c] = (lred[c] + lred[NC + c]) + (lred[2 * NC + c] + lred[3 * NC + c]);
+    if (qd == 0 && lane == 0) {
+      vref_s[g] = vref;
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) unset_s[g * C::NB + n] = unset[n];
     }
-    named_bar_sync(1 + hf, 128);
+    const bool bad = bar_red_or(3, 256, !ok);  // both warpgroups
+    // each warpgroup writes half of the rows; its first 64 threads find their
+    // factors (and with sets the weights of the two O^T)
+    constexpr int EC = NC / 2;
+    const int e0 = g * EC;
+    const int gt = (int)threadIdx.x & 127;
+    if (!bad && gt < EC) {
+      const int c = e0 + gt;
+      float m[2], l[2], w[2];
+      float M = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < C::kSets; ++s) {
+        const int gs = C::kSets == 2 ? s : g, cc = C::kSets == 2 ? c : gt;
+        const float* rr = red + gs * 4 * C::CP + cc;
+        l[s] = (rr[0] + rr[C::CP]) + (rr[2 * C::CP] + rr[3 * C::CP]);
+        const bool open = (unset_s[gs * C::NB + cc / C::BS] >> (cc % C::BS)) & 1u;
+        // an open row with a sum of NaN (a NaN score) must still count
+        m[s] = open ? (l[s] != l[s] ? 0.f : -INFINITY) : -nm[gs * C::CP + cc];
+        M = fmaxf(M, m[s]);
+      }
+      float Ls = 0.f;
+#pragma unroll
+      for (int s = 0; s < C::kSets; ++s) {
+        w[s] = m[s] == -INFINITY ? 0.f : exp2f(m[s] - M);
+        if (w[s] != 0.f) Ls += w[s] * l[s];
+      }
+      const float inv = p.P == 1 ? (Ls == 0.f ? 0.f : 1.f / Ls) : 1.f;
+#pragma unroll
+      for (int s = 0; s < C::kSets; ++s) {
+        const int gs = C::kSets == 2 ? s : g;
+        fo[s * NC + c] = w[s] * inv * vref_s[gs];
+      }
+      if (p.P > 1 && crow[c] >= 0)
+        p.pml[((size_t)bk * p.P + chunk) * p.R + row0 + c] = make_float2(M, Ls);
+    }
+    named_bar_sync(bar_id, 128);
     if (!bad) {
       tc_fence_after();
       // TMEM lane = position 8 w + 2 jj + h of dim 8 w + jj + 4 h
       const int jj = (key >> 1) & 3;
       const int dim = (key & ~7) + jj + 4 * (key & 1);
       const float unit = (jj & 1) ? 0x1p13f : 0x1p17f;  // 2^20 or 2^24, times 2^-7
-#pragma unroll
-      for (int s = 0; s < C::NSB; ++s) {
+      __nv_bfloat16* ob = p.out + (size_t)b * p.N * p.Hq * DH + dim;
+      float* pb = p.po + (((size_t)bk * p.P + chunk) * p.R + row0) * DH + dim;
 #pragma unroll 1
-        for (int c0 = 0; c0 < C::SB; c0 += 8) {
-          const int col = hf * C::CP + s * C::SB + c0;
-          if (row0 + col >= p.R) break;  // warp-uniform
-          float o8[8];
-          tmem_ld8(tmem + lane_base + (uint32_t)col, o8);
+      for (int c0 = e0; c0 < e0 + EC; c0 += 8) {
+        if (row0 + c0 >= p.R) break;  // warp-uniform
+        float o8[8], x8[8];
+        tmem_ld8(tmem + lane_base + (uint32_t)c0, o8);
+        if constexpr (C::kSets == 2) tmem_ld8(tmem + lane_base + (uint32_t)(NC + c0), x8);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = row0 + col + e;
-            if (r >= p.R) continue;
-            const float o = o8[e] * unit * vref[s];
-            const float l = lsum[col + e];
-            if (p.P == 1) {
-              const int node = r / p.G, g = r - node * p.G;
-              p.out[(((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH + dim] =
-                  __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-            } else {
-              const size_t prow = ((size_t)bk * p.P + chunk) * p.R + r;
-              p.po[prow * DH + dim] = o;
-              if (key == 0) {
-                const float m = nm[col + e];
-                // a sum of NaN must reach the merge, which skips m = -inf
-                p.pml[prow] = make_float2(m == 1e30f ? (l != l ? 0.f : -INFINITY) : (m != m ? 0.f : -m), l);
-              }
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const int r = crow[c0 + e];
+          if (r < 0) continue;
+          // a factor of 0: that warpgroup saw no key of the row (its O^T may be unwritten)
+          float o = fo[c0 + e] == 0.f ? 0.f : o8[e] * unit * fo[c0 + e];
+          if constexpr (C::kSets == 2)
+            o += fo[NC + c0 + e] == 0.f ? 0.f : x8[e] * unit * fo[NC + c0 + e];
+          if (p.P == 1) ob[(size_t)r * DH] = __float2bfloat16_rn(o);
+          else pb[(size_t)(c0 + e) * DH] = o;
         }
       }
     }
@@ -750,6 +824,18 @@ int packed_run(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& 
 }
 
 }  // namespace
+
+int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear) {
+  const unsigned zero = 0u;
+  *status = *site = 0u;
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_dev_status, sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(site, g_dev_debug_site, sizeof(unsigned));
+  if (e == cudaSuccess && clear) {
+    e = cudaMemcpyToSymbol(g_dev_status, &zero, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_dev_debug_site, &zero, sizeof(unsigned));
+  }
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "device status");
+}
 
 bool attention_packed_tc_eligible(int dtype, int dh) { return dtype == MEDUSA_BF16 && dh == DH; }
 

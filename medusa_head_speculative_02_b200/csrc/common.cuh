@@ -13,9 +13,16 @@ namespace medusa {
 // Set by a bounded device wait that ran out (DEV_TIMEOUT) or, in MEDUSA_DEBUG
 // builds, by a failed index check (DEV_BOUNDS); read by medusa_device_status().
 enum : unsigned { DEV_OK = 0u, DEV_TIMEOUT = 1u, DEV_BOUNDS = 2u };
+// A source compiled on its own (MEDUSA_OWN_STATUS; no relocatable device code)
+// has words of its own, which medusa_device_status reads too.
+#ifdef MEDUSA_OWN_STATUS
+static __device__ unsigned int g_dev_status = 0u;
+static __device__ unsigned int g_dev_debug_site = 0u;
+#else
 extern __device__ unsigned int g_dev_status;
 // First failing check site of a MEDUSA_DEBUG build (0: none).
 extern __device__ unsigned int g_dev_debug_site;
+#endif
 
 // Check sites of the MEDUSA_DEBUG build (reported by medusa_debug_site()).
 enum : unsigned {
@@ -371,6 +378,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// Store of 16 32-bit columns without its completion wait (tmem_wait_st).
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 // tcgen05.mma kind::f16 with the A operand in TMEM (K-major rows, two bf16
 // per 32-bit column) and B described in shared memory.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
@@ -399,6 +419,46 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
       : "r"(taddr)
       : "memory");
   return __uint_as_float(r);
+}
+// The same MMAs and their commit for a whole warp in lockstep: one elected lane
+// issues.  With the loop around them warp-uniform (no lane test), descriptors
+// stay in uniform registers; behind a lane test each operand is first moved
+// out of a divergent register, and an MMA takes at least 97 cycles to issue
+// whatever its size (measured: M 128, K 16, A in TMEM: N 16 / 64 / 128 take
+// 10 / 32 / 64 cycles issued this way).
+__device__ __forceinline__ void umma_f16_warp(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts_warp(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+// mbar_wait by every lane of a warp; the same answer in all of them.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
 }
 // Named barrier over `n` threads that also ORs a predicate across them, so
 // every participant takes the same decision.
@@ -521,6 +581,17 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_addr, uint32_t
 // Instruction descriptor with the B operand MN-major (bit 16).
 __host__ __device__ constexpr uint32_t umma_idesc_bf16_f32_bmn(int M, int N) {
   return umma_idesc_bf16_f32(M, N) | (1u << 16);
+}
+// Registers per thread of a whole warpgroup from here on.  What reg_inc takes
+// must have been given up by reg_dec: the sum over the block stays within the
+// registers it was launched with.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Programmatic dependent launch: wait until every kernel this one depends on
 // has completed and its memory is visible; let the next kernel in the stream

@@ -197,6 +197,7 @@ struct AttnExtArgs {
 bool attention_packed_tc_eligible(int dtype, int dh);
 size_t attention_packed_tc_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap,
                                      int window, int sinks);
+int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear);
 int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStream_t st);
 // Most slots a sequence's nodes can see.
 long long ext_max_keys(int Lcap, int N, int window, int sinks);

@@ -289,6 +289,11 @@ int medusa_device_status(int* status, int clear) {
     if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_dev_debug_site, &z, sizeof(z));
     if (e != cudaSuccess) return cuda_fail(e, "clear device status");
   }
+  unsigned int v2 = 0, site2 = 0;  // the words of the source compiled on its own
+  const int rc = attention_packed_tc_status(&v2, &site2, clear != 0);
+  if (rc) return rc;
+  v |= v2;
+  if (site == 0) site = site2;
   if (v & DEV_BOUNDS) {
     *status = MEDUSA_ERR_BOUNDS;
     fail(MEDUSA_ERR_BOUNDS, "device index check failed, first at site " + std::to_string(site));
