@@ -384,6 +384,8 @@ size_t attention_ext_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int
   if (!packed && window <= 0) return attention_workspace(t, B, Hq, Hkv, dh, Lcap, dtype);
   if (!packed && attention_tc_eligible(dtype, dh, Hq, Hkv))
     return window_tc_plan(t, B, Hq, Hkv, dh, Lcap, window, sinks).total;
+  if (packed && attention_packed_rows_eligible(dtype, dh, t->N * (Hq / Hkv)))
+    return attention_packed_rows_workspace(t, B, Hq, Hkv, Lcap, window, sinks);
   if (packed && attention_packed_tc_eligible(dtype, dh))
     return attention_packed_tc_workspace(t, B, Hq, Hkv, Lcap, window, sinks);
   return simt_plan(t, B, Hq, Hkv, dh, Lcap, window, sinks).total;
@@ -401,6 +403,8 @@ int attention_ext_launch(const AttnExtArgs& x, cudaStream_t st) {
     if (rc || p.sh.P == 1 || p.sh.fuse) return rc;
     return attention_combine_launch(a, po, pml, p.sh.P, st);
   }
+  if (x.packed && attention_packed_rows_eligible(a.dtype, a.dh, a.tree->N * (a.Hq / a.Hkv)))
+    return attention_packed_rows_launch(a, *x.packed, st);
   if (x.packed && attention_packed_tc_eligible(a.dtype, a.dh))
     return attention_packed_tc_launch(a, *x.packed, st);
   return simt_launch(x, st);

@@ -199,6 +199,11 @@ size_t attention_packed_tc_workspace(const medusa_tree* t, int B, int Hq, int Hk
                                      int window, int sinks);
 int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear);
 int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStream_t st);
+// the same for at most 16 query rows per kv-head (csrc/attention_packed_rows.cu)
+bool attention_packed_rows_eligible(int dtype, int dh, int rows);
+size_t attention_packed_rows_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap,
+                                       int window, int sinks);
+int attention_packed_rows_launch(const AttnArgs& a, const PackedCache& c, cudaStream_t st);
 // Most slots a sequence's nodes can see.
 long long ext_max_keys(int Lcap, int N, int window, int sinks);
 size_t attention_ext_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
