@@ -52,7 +52,7 @@ struct RowsParams {
   const int32_t* L;
   const uint32_t* anc;
   const int32_t* depth;
-  int N, W, K, Hq, Hkv, G, Lcap, R, P, window, sinks;
+  int B, N, W, K, Hq, Hkv, G, Lcap, R, P, window, sinks;
   float scale2;
   __nv_bfloat16* out;
   float* po;
@@ -112,8 +112,21 @@ __global__ void __launch_bounds__(32 * kWarps, NQ == 1 ? 4 : 3)
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int chunk = blockIdx.x % p.P, bk = blockIdx.x / p.P;
-  const int b = bk / p.Hkv, kvh = bk - b * p.Hkv;
+  const int chunk = blockIdx.x % p.P, place = blockIdx.x / p.P;
+  // the longest sequences start first (up to 32 sequences; ties by index)
+  int b = place / p.Hkv;
+  const int kvh = place - b * p.Hkv;
+  if (p.B > 1 && p.B <= 32) {
+    const int mine = lane < p.B ? p.L[lane] : -1;
+    int rank = 0;
+    for (int i = 0; i < p.B; ++i) {
+      const int x = __shfl_sync(0xffffffffu, mine, i);
+      rank += (x > mine || (x == mine && i < lane)) ? 1 : 0;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, lane < p.B && rank == b);
+    b = __ffs(who) - 1;
+  }
+  const int bk = b * p.Hkv + kvh;
   const int Lb = p.L[b];
   const bool seq_ok = Lb >= 0 && (long long)Lb + p.N <= p.Lcap;
 
@@ -127,6 +140,51 @@ __global__ void __launch_bounds__(32 * kWarps, NQ == 1 ? 4 : 3)
   }
   const int j0 = (int)((long long)nb * chunk / p.P);
   const int T = (int)((long long)nb * (chunk + 1) / p.P) - j0;
+
+  // this lane's pieces of a group: 16 bytes of keys lane / 4 and + 8 of K and
+  // of V; V's rows and pieces are placed so that the 8-byte reads of keys
+  // 4 t + i fall in different banks
+  const size_t row0 = (size_t)bk * p.Lcap;
+  const uint32_t ring_a = smem_u32(smem) + warp * (kStages * kGroupBytes);
+  const uint8_t* ring = smem + warp * (kStages * kGroupBytes);
+  const int ck = lane >> 2, cc = lane & 3;
+  const uint8_t* ksrc = p.kc + row0 * (DH / 2) + lane * 16;
+  const uint8_t* vsrc = p.vc + row0 * (DH / 2) + lane * 16;
+  const uint8_t* psrc = (const uint8_t*)((lane < 4 ? p.kp : p.vp) + row0) + (lane & 3) * 16;
+  const uint32_t kdst = lane * 16;
+  const uint32_t vdst = 1024 + (ck ^ ((ck >> 2) & 1)) * 64 + cc * 16;
+  const uint32_t vdst8 = 1024 + ((ck + 8) ^ ((ck >> 2) & 1)) * 64 + (cc ^ 2) * 16;
+  auto slot0 = [&](int j) {  // first slot of this warp's group in block j0 + j
+    const int jj = j0 + j;
+    return (jj < nh ? jj : jj - nh + b_lo) * KB + warp * 16;
+  };
+  auto issue = [&](int j) {
+    if (j < T) {
+      const int s0 = slot0(j);
+      const uint32_t dst = ring_a + (j % kStages) * kGroupBytes;
+      const size_t off = (size_t)s0 * (DH / 2);
+      if (s0 + 16 <= p.Lcap) {
+        cp16(dst + kdst, ksrc + off);
+        cp16(dst + kdst + 512, ksrc + off + 512);
+        cp16(dst + vdst, vsrc + off);
+        cp16(dst + vdst8, vsrc + off + 512);
+        if (lane < 8) cp16(dst + 2048 + lane * 16, psrc + (size_t)s0 * 4);
+      } else {
+      const bool l0 = s0 + ck < p.Lcap, l8 = s0 + ck + 8 < p.Lcap;  // past the cache: zeros
+      cp16(dst + kdst, l0 ? ksrc + off : p.kc, l0);
+      cp16(dst + kdst + 512, l8 ? ksrc + off + 512 : p.kc, l8);
+      cp16(dst + vdst, l0 ? vsrc + off : p.vc, l0);
+      cp16(dst + vdst8, l8 ? vsrc + off + 512 : p.vc, l8);
+      if (lane < 8) {  // 16 K words, 16 V words (Lcap is a multiple of 4)
+        const bool lp = s0 + (lane & 3) * 4 < p.Lcap;
+        cp16(dst + 2048 + lane * 16, lp ? psrc + (size_t)s0 * 4 : (const uint8_t*)p.kp, lp);
+      }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  for (int j = 0; j < kStages - 1; ++j) issue(j);  // in flight while Q is prepared
 
   // Q fragments (row 8 n + g): pair j of this lane's word wi is dims
   // 8 (4 t4 + wi) + j, + 4
@@ -190,49 +248,6 @@ __global__ void __launch_bounds__(32 * kWarps, NQ == 1 ? 4 : 3)
     qsum[n][1] = __shfl_sync(0xffffffffu, x, 8 * t4 + 4);
   }
 
-  // this lane's pieces of a group: 16 bytes of keys lane / 4 and + 8 of K and
-  // of V; V's rows and pieces are placed so that the 8-byte reads of keys
-  // 4 t + i fall in different banks
-  const size_t row0 = (size_t)bk * p.Lcap;
-  const uint32_t ring_a = smem_u32(smem) + warp * (kStages * kGroupBytes);
-  const uint8_t* ring = smem + warp * (kStages * kGroupBytes);
-  const int ck = lane >> 2, cc = lane & 3;
-  const uint8_t* ksrc = p.kc + row0 * (DH / 2) + lane * 16;
-  const uint8_t* vsrc = p.vc + row0 * (DH / 2) + lane * 16;
-  const uint8_t* psrc = (const uint8_t*)((lane < 4 ? p.kp : p.vp) + row0) + (lane & 3) * 16;
-  const uint32_t kdst = lane * 16;
-  const uint32_t vdst = 1024 + (ck ^ ((ck >> 2) & 1)) * 64 + cc * 16;
-  const uint32_t vdst8 = 1024 + ((ck + 8) ^ ((ck >> 2) & 1)) * 64 + (cc ^ 2) * 16;
-  auto slot0 = [&](int j) {  // first slot of this warp's group in block j0 + j
-    const int jj = j0 + j;
-    return (jj < nh ? jj : jj - nh + b_lo) * KB + warp * 16;
-  };
-  auto issue = [&](int j) {
-    if (j < T) {
-      const int s0 = slot0(j);
-      const uint32_t dst = ring_a + (j % kStages) * kGroupBytes;
-      const size_t off = (size_t)s0 * (DH / 2);
-      if (s0 + 16 <= p.Lcap) {
-        cp16(dst + kdst, ksrc + off);
-        cp16(dst + kdst + 512, ksrc + off + 512);
-        cp16(dst + vdst, vsrc + off);
-        cp16(dst + vdst8, vsrc + off + 512);
-        if (lane < 8) cp16(dst + 2048 + lane * 16, psrc + (size_t)s0 * 4);
-      } else {
-      const bool l0 = s0 + ck < p.Lcap, l8 = s0 + ck + 8 < p.Lcap;  // past the cache: zeros
-      cp16(dst + kdst, l0 ? ksrc + off : p.kc, l0);
-      cp16(dst + kdst + 512, l8 ? ksrc + off + 512 : p.kc, l8);
-      cp16(dst + vdst, l0 ? vsrc + off : p.vc, l0);
-      cp16(dst + vdst8, l8 ? vsrc + off + 512 : p.vc, l8);
-      if (lane < 8) {  // 16 K words, 16 V words (Lcap is a multiple of 4)
-        const bool lp = s0 + (lane & 3) * 4 < p.Lcap;
-        cp16(dst + 2048 + lane * 16, lp ? psrc + (size_t)s0 * 4 : (const uint8_t*)p.kp, lp);
-      }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
   // O^T: [dim block][row block]; fragment register 2 i + e is dim row g + 8 i,
   // query row 8 n + 2 t4 + e
   float o[8][NQ][4];
@@ -255,7 +270,6 @@ __global__ void __launch_bounds__(32 * kWarps, NQ == 1 ? 4 : 3)
   const int m_lo = p.window > 0 && wl >= 0 ? (int)wl : -1;
   const int kg = 4 * (g >> 1) + (g & 1);  // key of row g of the K fragment; row g + 8 is kg + 2
 
-  for (int j = 0; j < kStages - 1; ++j) issue(j);
   for (int j = 0; j < T; ++j) {
     issue(j + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -516,11 +530,17 @@ RowsPlan rows_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, int w
   p.R = t->N * (Hq / Hkv);
   const long long units = (long long)B * Hkv;
   const long long nb = (ext_max_keys(Lcap, t->N, window, sinks) + KB - 1) / KB + (window > 0 ? 1 : 0);
-  // about 4 waves of resident CTAs (sequences differ in length), 4 blocks a CTA at least
-  const long long want = units > 0 ? ((p.R <= 8 ? 16LL : 12LL) * num_sms() + units - 1) / units : 1;
-  long long P = want < nb / 4 ? want : nb / 4;
-  if (P < 1) P = 1;
-  if (P > 128) P = 128;
+  // key chunks: least (waves of resident CTAs) x (blocks of a CTA + its start
+  // and end, about 4 blocks' time)
+  const long long slots = (p.R <= 8 ? 4LL : 3LL) * num_sms();
+  long long best = 0, P = 1;
+  for (long long x = 1; units > 0 && x <= 64 && x <= nb; ++x) {
+    const long long cost = ((units * x + slots - 1) / slots) * ((nb + x - 1) / x + 4 + (x > 1 ? 2 : 0));
+    if (best == 0 || cost < best) {
+      best = cost;
+      P = x;
+    }
+  }
   p.P = (int)P;
   p.ctas = units * p.P;
   WsCarver w;
@@ -567,6 +587,7 @@ int attention_packed_rows_launch(const AttnArgs& a, const PackedCache& c, cudaSt
   p.L = a.L;
   p.anc = t->d_anc;
   p.depth = t->d_depth;
+  p.B = a.B;
   p.N = t->N;
   p.W = t->W;
   p.K = t->K;
