@@ -394,23 +394,49 @@ def medusa_kv_compact(k_cache, v_cache, prefix_len, accept_len, accept_nodes, K:
 
 
 # ---------------------------------------------------------------- 4-bit cache, sliding window
-def _same_device(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+# These calls are made once per layer and step on small inputs, where the host's
+# part is most of the time: the checks are one expression per tensor (the
+# message is worked out only on failure), pointers go as integers, and the
+# device is switched only when it is not the current one.
+_I32 = torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _i32(t, name: str, shape, dev) -> None:
-    _need(t, name, torch.int32, shape)
-    _same_device(dev, **{name: t})
+def _refuse(t, name: str, dtype, shape, dev: int):
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _out_like(out, name: str, dtype, shape, dev):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(out, name, dtype, shape)
-    _same_device(dev, **{name: out})
-    return out
+def _chk(t, name: str, dtype, shape, dev: int) -> int:
+    """Data pointer of a contiguous tensor of this dtype and shape on CUDA
+    device `dev`; raises otherwise."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or \
+            t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _chk(t, name, dtype, shape, dev)
+
+
+def _dev(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(dev: int, fn, where: str, *args) -> None:
+    """fn(*args, stream) with device `dev` current, on its current stream."""
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc:
+        L.check(rc, where)
 
 
 class PackedCache:
@@ -420,23 +446,23 @@ class PackedCache:
     then stands for zeros)."""
 
     __slots__ = ("k_codes", "k_par", "v_codes", "v_par", "layers", "B", "Hkv", "Lcap", "dh",
-                 "device", "_ptrs")
+                 "device", "_idx", "_ptrs")
 
     def __init__(self, k_codes, k_par, v_codes, v_par):
         _need(k_codes, "k_codes", torch.uint8)
         shape = tuple(k_codes.shape)
         if len(shape) not in (4, 5):
             raise ValueError("k_codes must be [B][Hkv][Lcap][dh/2] or [layers][B][Hkv][Lcap][dh/2]")
-        _need(v_codes, "v_codes", torch.uint8, shape)
-        _need(k_par, "k_par", torch.bfloat16, shape[:-1] + (2,))
-        _need(v_par, "v_par", torch.bfloat16, shape[:-1] + (2,))
-        _same_device(k_codes.device, k_par=k_par, v_codes=v_codes, v_par=v_par)
+        self._idx = dev = k_codes.get_device()
+        par = shape[:-1] + (2,)
+        self._ptrs = (k_codes.data_ptr(), _chk(k_par, "k_par", torch.bfloat16, par, dev),
+                      _chk(v_codes, "v_codes", torch.uint8, shape, dev),
+                      _chk(v_par, "v_par", torch.bfloat16, par, dev))
         self.k_codes, self.k_par, self.v_codes, self.v_par = k_codes, k_par, v_codes, v_par
         self.layers = shape[0] if len(shape) == 5 else None
         self.B, self.Hkv, self.Lcap = shape[-4:-1]
         self.dh = 2 * shape[-1]
         self.device = k_codes.device
-        self._ptrs = (_ptr(k_codes), _ptr(k_par), _ptr(v_codes), _ptr(v_par))
 
     @classmethod
     def empty(cls, B: int, Hkv: int, Lcap: int, dh: int, device="cuda", layers=None):
@@ -460,18 +486,12 @@ def medusa_kv_pack(k, v, cache: PackedCache, start, count=None) -> None:
     """Stores K/V rows k, v [B][T][Hkv][dh] in the 4-bit cache: token t <
     count[b] (count None: all T) of sequence b at slot start[b] + t."""
     cache._single()
-    B, T = k.shape[0], k.shape[1]
-    _need(k, "k", k.dtype, (cache.B, T, cache.Hkv, cache.dh))
-    _need(v, "v", k.dtype, k.shape)
-    dev = cache.device
-    _same_device(dev, k=k, v=v)
-    _i32(start, "start", (B,), dev)
-    if count is not None:
-        _i32(count, "count", (B,), dev)
-    with torch.cuda.device(dev):
-        L.check(L.lib().medusa_kv_pack(_ptr(k), _ptr(v), _dt(k), _ptr(start), _ptr(count), B, T,
-                                       cache.Hkv, cache.dh, cache.Lcap, *cache._ptrs,
-                                       _stream(dev)), "medusa_kv_pack")
+    dev, dt, B, T = cache._idx, _dt(k), cache.B, k.shape[1]
+    shape = (B, T, cache.Hkv, cache.dh)
+    _call(dev, L.lib().medusa_kv_pack, "medusa_kv_pack", _chk(k, "k", k.dtype, shape, dev),
+          _chk(v, "v", k.dtype, shape, dev), dt, _chk(start, "start", _I32, (B,), dev),
+          _opt(count, "count", _I32, (B,), dev), B, T, cache.Hkv, cache.dh, cache.Lcap,
+          *cache._ptrs)
 
 
 def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = torch.bfloat16,
@@ -481,17 +501,17 @@ def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = tor
     cache._single()
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    dev = cache.device
-    shape = (cache.B, int(T), cache.Hkv, cache.dh)
-    _i32(start, "start", (cache.B,), dev)
-    if count is not None:
-        _i32(count, "count", (cache.B,), dev)
-    k, v = out if out is not None else (None, None)
-    k, v = _out_like(k, "k", dtype, shape, dev), _out_like(v, "v", dtype, shape, dev)
-    with torch.cuda.device(dev):
-        L.check(L.lib().medusa_kv_unpack(*cache._ptrs, _ptr(start), _ptr(count), cache.B, int(T),
-                                         cache.Hkv, cache.dh, cache.Lcap, _DT[dtype], _ptr(k),
-                                         _ptr(v), _stream(dev)), "medusa_kv_unpack")
+    dev, B, T = cache._idx, cache.B, int(T)
+    shape = (B, T, cache.Hkv, cache.dh)
+    if out is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        k, v = out
+    _call(dev, L.lib().medusa_kv_unpack, "medusa_kv_unpack", *cache._ptrs,
+          _chk(start, "start", _I32, (B,), dev), _opt(count, "count", _I32, (B,), dev), B, T,
+          cache.Hkv, cache.dh, cache.Lcap, _DT[dtype], _chk(k, "k", dtype, shape, dev),
+          _chk(v, "v", dtype, shape, dev))
     return k, v
 
 
@@ -499,67 +519,70 @@ def medusa_kv_compact_packed(cache: PackedCache, prefix_len, accept_len, accept_
                              new_len=None):
     """Compaction of the accepted path in a 4-bit cache (every layer of one
     with a layer axis, in one launch); returns new_len [B]."""
-    dev = cache.device
-    _i32(prefix_len, "prefix_len", (cache.B,), dev)
-    _i32(accept_len, "accept_len", (cache.B,), dev)
-    _i32(accept_nodes, "accept_nodes", (cache.B, K + 1), dev)
-    new_len = _out_like(new_len, "new_len", torch.int32, (cache.B,), dev)
-    with torch.cuda.device(dev):
-        L.check(L.lib().medusa_kv_compact_packed(
-            *cache._ptrs, 1 if cache.layers is None else cache.layers, _ptr(prefix_len),
-            _ptr(accept_len), _ptr(accept_nodes), cache.B, cache.Hkv, cache.dh, cache.Lcap, K,
-            _ptr(new_len), _stream(dev)), "medusa_kv_compact_packed")
+    dev, B = cache._idx, cache.B
+    if new_len is None:
+        new_len = torch.empty(B, dtype=_I32, device=cache.device)
+    _call(dev, L.lib().medusa_kv_compact_packed, "medusa_kv_compact_packed", *cache._ptrs,
+          1 if cache.layers is None else cache.layers,
+          _chk(prefix_len, "prefix_len", _I32, (B,), dev),
+          _chk(accept_len, "accept_len", _I32, (B,), dev),
+          _chk(accept_nodes, "accept_nodes", _I32, (B, K + 1), dev), B, cache.Hkv, cache.dh,
+          cache.Lcap, K, _chk(new_len, "new_len", _I32, (B,), dev))
     return new_len
 
 
 def attention_packed_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
                                     window: int = 0, sinks: int = 0) -> int:
-    return int(L.lib().medusa_tree_attention_packed_workspace_size(
-        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks))
+    return L.lib().medusa_tree_attention_packed_workspace_size(
+        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks)
 
 
 def attention_window_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
                                     window: int, sinks: int = 0) -> int:
-    return int(L.lib().medusa_tree_attention_window_workspace_size(
-        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks))
+    return L.lib().medusa_tree_attention_window_workspace_size(
+        tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks)
 
 
-def _ext_args(q, tree, prefix_len, dev, out, ws, size):
-    """Checked output and workspace of the windowed / 4-bit attention calls
-    (the device is current)."""
+def _ext_buffers(size, q, tree, Hkv, Lcap, window, sinks, dev, out, ws):
+    """Output (checked or made), workspace and its bytes; the plan behind the
+    size needs device `dev` current."""
     B, N, Hq, dh = q.shape
     if N != tree.N:
         raise ValueError(f"q has {N} nodes, tree has {tree.N}")
-    _i32(prefix_len, "prefix_len", (B,), dev)
-    out = _out_like(out, "out", q.dtype, q.shape, dev)
-    need = size()
-    if ws is None or ws.numel() * ws.element_size() < need:
-        ws = _ws(need, dev)
+    if out is None:
+        out = torch.empty_like(q)
     else:
-        _same_device(dev, ws=ws)
-    return out, ws, ws.numel() * ws.element_size()
+        _chk(out, "out", q.dtype, q.shape, dev)
+    if torch._C._cuda_getDevice() == dev:
+        need = size(tree, B, Hq, Hkv, dh, Lcap, q.dtype, window, sinks)
+    else:
+        with torch.cuda.device(dev):
+            need = size(tree, B, Hq, Hkv, dh, Lcap, q.dtype, window, sinks)
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous on cuda:{dev}")
+        have = ws.numel() * ws.element_size()
+        if have >= need:
+            return out, ws, have
+    ws = _ws(need, q.device)
+    return out, ws, ws.numel()
 
 
 def medusa_tree_attention_window(q, k_cache, v_cache, prefix_len, tree: Tree, scale: float,
                                  window: int, sinks: int = 0, out=None, ws=None):
     """medusa_tree_attention restricted to a sliding window of `window`
     positions (0: none) and the first `sinks` positions."""
-    B, N, Hq, dh = q.shape
+    dev, dt = _dev(q, "q"), _dt(q)
+    B, _, Hq, dh = q.shape
     Lcap, Hkv = k_cache.shape[1], k_cache.shape[2]
-    dt = _dt(q)
-    dev = q.device
-    _need(q, "q", q.dtype)
-    _need(k_cache, "k_cache", q.dtype, (B, Lcap, Hkv, dh))
-    _need(v_cache, "v_cache", q.dtype, (B, Lcap, Hkv, dh))
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache)
-    with torch.cuda.device(dev):
-        out, ws, nws = _ext_args(q, tree, prefix_len, dev, out, ws,
-                                 lambda: attention_window_workspace_size(
-                                     tree, B, Hq, Hkv, dh, Lcap, q.dtype, window, sinks))
-        L.check(L.lib().medusa_tree_attention_window(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), tree.handle, B, Hq, Hkv, dh,
-            Lcap, float(scale), dt, window, sinks, _ptr(out), _ptr(ws), nws, _stream(dev)),
-            "medusa_tree_attention_window")
+    shape = (B, Lcap, Hkv, dh)
+    out, ws, nws = _ext_buffers(attention_window_workspace_size, q, tree, Hkv, Lcap, window, sinks,
+                                dev, out, ws)
+    _call(dev, L.lib().medusa_tree_attention_window, "medusa_tree_attention_window",
+          _chk(q, "q", q.dtype, q.shape, dev), _chk(k_cache, "k_cache", q.dtype, shape, dev),
+          _chk(v_cache, "v_cache", q.dtype, shape, dev),
+          _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq, Hkv, dh, Lcap,
+          scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws)
     return out
 
 
@@ -568,19 +591,13 @@ def medusa_tree_attention_packed(q, cache: PackedCache, prefix_len, tree: Tree, 
     """Tree attention over a 4-bit cache, full (window 0) or with a sliding
     window and sinks.  A one-node tree is single-token decoding."""
     cache._single()
-    B, N, Hq, dh = q.shape
     dt = _dt(q)
-    dev = q.device
-    _need(q, "q", q.dtype, (cache.B, N, Hq, cache.dh))
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
-    with torch.cuda.device(dev):
-        out, ws, nws = _ext_args(q, tree, prefix_len, dev, out, ws,
-                                 lambda: attention_packed_workspace_size(
-                                     tree, B, Hq, cache.Hkv, dh, cache.Lcap, q.dtype, window,
-                                     sinks))
-        L.check(L.lib().medusa_tree_attention_packed(
-            _ptr(q), *cache._ptrs, _ptr(prefix_len), tree.handle, B, Hq, cache.Hkv, dh,
-            cache.Lcap, float(scale), dt, window, sinks, _ptr(out), _ptr(ws), nws,
-            _stream(dev)), "medusa_tree_attention_packed")
+    dev, Hkv, Lcap = cache._idx, cache.Hkv, cache.Lcap
+    B, N, Hq, dh = q.shape
+    pq = _chk(q, "q", q.dtype, (cache.B, N, Hq, cache.dh), dev)
+    out, ws, nws = _ext_buffers(attention_packed_workspace_size, q, tree, Hkv, Lcap, window, sinks,
+                                dev, out, ws)
+    _call(dev, L.lib().medusa_tree_attention_packed, "medusa_tree_attention_packed", pq,
+          *cache._ptrs, _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq, Hkv,
+          dh, Lcap, scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws)
     return out
