@@ -100,6 +100,7 @@ struct PackedParams {
   const int32_t* L;
   const uint32_t* anc;
   const int32_t* depth;
+  const int32_t* parent;
   int B, N, W, K, Hq, Hkv, G, Lcap, R, groups, P, window, sinks;
   float scale2;  // softmax scale * log2(e)
   __nv_bfloat16* out;
@@ -774,8 +775,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   }
 }
 
+#include "attention_packed_pair.cuh"
+
 struct PackedPlan {
-  int NC, R, groups, P;
+  int NC, R, groups, P;  // NC = 256: two query tiles a CTA (attention_packed_pair.cuh)
   long long ctas;
   size_t off_o, off_ml, total;
 };
@@ -784,7 +787,7 @@ PackedPlan packed_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, i
                        int sinks) {
   PackedPlan p;
   p.R = t->N * (Hq / Hkv);
-  p.NC = p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
+  p.NC = p.R <= 32 ? 32 : p.R <= 64 ? 64 : p.R <= 128 ? 128 : 256;
   p.groups = (p.R + p.NC - 1) / p.NC;
   const long long units = (long long)B * Hkv * p.groups;
   const long long T = (ext_max_keys(Lcap, t->N, window, sinks) + BK - 1) / BK + (window > 0 ? 1 : 0);
@@ -837,6 +840,20 @@ int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear) {
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "device status");
 }
 
+namespace {
+int pair_run(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& kp,
+             const CUtensorMap& vp, const PackedParams& p, long long ctas, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  int rc = ensure_max_smem(tree_attn_packed_pair_kernel, (int)PairCfg::kSmem, done,
+                           "cudaFuncSetAttribute(tree_attn_packed_pair_kernel)");
+  if (rc) return rc;
+  cudaError_t e = launch_pdl(tree_attn_packed_pair_kernel, dim3((unsigned)ctas),
+                             dim3(PairCfg::kThreads), PairCfg::kSmem, st, kc, vc, kp, vp, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "tree_attn_packed_pair_kernel launch");
+}
+}  // namespace
+
 bool attention_packed_tc_eligible(int dtype, int dh) { return dtype == MEDUSA_BF16 && dh == DH; }
 
 size_t attention_packed_tc_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap,
@@ -874,6 +891,7 @@ int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStre
   p.L = a.L;
   p.anc = t->d_anc;
   p.depth = t->d_depth;
+  p.parent = t->d_parent;
   p.B = a.B;
   p.N = t->N;
   p.W = t->W;
@@ -893,10 +911,10 @@ int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStre
   p.pml = (float2*)((uint8_t*)a.ws + pl.off_ml);
   int rc;
   switch (pl.NC) {
-    case 16: rc = packed_run<16>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
     case 32: rc = packed_run<32>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
     case 64: rc = packed_run<64>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
-    default: rc = packed_run<128>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
+    case 128: rc = packed_run<128>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
+    default: rc = pair_run(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
   }
   if (rc || pl.P == 1) return rc;
   return attention_combine_launch(a, p.po, p.pml, pl.P, st);
