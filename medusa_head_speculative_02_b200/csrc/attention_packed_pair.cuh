@@ -31,10 +31,27 @@ struct PairCfg {
   static constexpr uint32_t oV = oK + 2 * kTile;
   static constexpr uint32_t oRing = oV + 2 * kTile;
   static constexpr uint32_t oScale = oRing + kItems * kItem;
-  static constexpr uint32_t oMisc = oScale + 4 * 2 * BK * 4;
+  static constexpr uint32_t oMisc = oScale + 4 * BK * 4;
   static constexpr size_t kSmem = 1024 + oMisc + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
+
+// The 8 codes of a word as four fp16 pairs of scale * (code - zero), rounded
+// once: 1024 + code and 1024 + 16 code are fp16 numbers by their bits, z1 =
+// -(1024 + zero) and z16 = -(1024 + 16 zero) bring them to code - zero and 16
+// times it, a1 and a16 = a1 / 16 are the scale.
+__device__ __forceinline__ void unpack_word_scaled(uint32_t w, __half2 z1, __half2 z16, __half2 a1,
+                                                   __half2 a16, uint32_t* r) {
+  const uint32_t v = w >> 8;
+  const uint32_t e[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                         (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&e[j]), (j & 1) ? z16 : z1),
+                              (j & 1) ? a16 : a1);
+    r[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
 
 // Visible keys of the 32 slots from s0 for a query row (node, depth): prefix
 // slots, ancestors, both within the row's window.
@@ -85,7 +102,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
   uint8_t* sK = sm + C::oK;
   uint8_t* sV = sm + C::oV;
   uint8_t* sRing = sm + C::oRing;
-  float* sScale = (float*)(sm + C::oScale);  // [4][K 128 | V 128]
+  float* sScale = (float*)(sm + C::oScale);  // [4][128]: K scale x softmax scale
   uint64_t* it_full = (uint64_t*)(sm + C::oMisc);  // [kItems]
   uint64_t* it_empty = it_full + C::kItems;  // [kItems]
   uint64_t* k_ready = it_empty + C::kItems;  // [2]
@@ -270,7 +287,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         const uint32_t tOq = tmem + 256u + (uint32_t)q * 128u;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16_ts_warp(tOq, aP + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8),
+          umma_f16_ts_warp(tOq, aP + (uint32_t)(kk * 8),
                            dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
                            (u > 0 || kk > 0) ? 1u : 0u);
         if (q == 1) umma_commit_warp(&v_empty[st]);  // both tiles have read V(u)
@@ -324,9 +341,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         vref = nref;
         if (t >= 2) ok = mbar_wait_warp(&k_empty[bf], prev, abort_flag);
         // softmax(t - 4) has read this scale buffer: S(t - 2) followed its P(t - 3)
-        sScale[(t & 3) * 2 * BK + key] = bf16_lo(par[key]) * cscale;
-        sScale[(t & 3) * 2 * BK + BK + key] =
-            bf16_lo(vp) * __uint_as_float((261u << 23) - __float_as_uint(vref));
+        // (a V row with no finite scale is stored as 0 and shows in the scores instead,
+        // so that it reaches the rows that see it and no other)
+        sScale[(t & 3) * BK + key] =
+            fabsf(bf16_lo(vp)) <= 3.3895314e38f ? bf16_lo(par[key]) * cscale : NAN;
         if (key == 0) {
           sGrow[t & 3] = grow;
           sRef[t & 3] = vref;
@@ -335,7 +353,20 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       uint32_t w[16];
       const uint8_t* row = sRing + st * C::kItem + key * 64;
       __half2 z24, z20;
-      zero_pairs(isV ? vp : ((const uint32_t*)(sRing + st * C::kItem + kCodeTile))[key], z24, z20);
+      __half2 a1, a16;
+      if (isV) {
+        const float z = fminf(fmaxf(bf16_hi(vp), 0.f), 15.f);
+        z24 = __float2half2_rn(-1024.f - z);
+        z20 = __float2half2_rn(-1024.f - 16.f * z);
+        // sv 2^10 / vref; none for a scale that is not finite or larger than
+        // those in use (a slot that no row sees)
+        float sv = bf16_lo(vp);
+        sv = fabsf(sv) <= vref ? sv * __uint_as_float((264u << 23) - __float_as_uint(vref)) : 0.f;
+        a1 = __float2half2_rn(sv);
+        a16 = __float2half2_rn(sv * 0.0625f);
+      } else {
+        zero_pairs(((const uint32_t*)(sRing + st * C::kItem + kCodeTile))[key], z24, z20);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<uint4*>(&w[4 * e]) = *reinterpret_cast<const uint4*>(row + ((e ^ sw) << 4));
@@ -347,7 +378,8 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           uint32_t r[4];
-          unpack_word(w[e], z24, z20, r);
+          if (isV) unpack_word_scaled(w[e], z24, z20, a1, a16, r);
+          else unpack_word(w[e], z24, z20, r);
           *reinterpret_cast<uint4*>(dst + (e >> 3) * kAtom + (((e & 7) ^ (key & 7)) << 4)) =
               make_uint4(r[0], r[1], r[2], r[3]);
         }
@@ -390,120 +422,98 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       if (live) {
         const int tile = tl.tile(j0 + t);
         const bool masked = tile >= m_hi || tile <= m_lo;
-        const float* sc = sScale + (t & 3) * 2 * BK;
-        float fv = sGrow[t & 3];  // growth of the value scale, once per tile
-#pragma unroll 1
-        for (int hf = 0; hf < 2 && ok; ++hf) {
-          float v[64];
-          tc_fence_after();
-          tmem_ld64(tS + (uint32_t)(hf * 64), v);
-          const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(sc + hf * 64);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 k = k2[c];
-            f2_unpack(f2_mul(f2_pack(v[4 * c], v[4 * c + 1]), k.x), v[4 * c], v[4 * c + 1]);
-            f2_unpack(f2_mul(f2_pack(v[4 * c + 2], v[4 * c + 3]), k.y), v[4 * c + 2], v[4 * c + 3]);
-          }
-          uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
-          if (masked) {
-            m0 = row_mask(tile * BK + hf * 64, Lb, node, depth, p);
-            m1 = row_mask(tile * BK + hf * 64 + 32, Lb, node, depth, p);
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              v[c] = ((c < 32 ? m0 : m1) >> (c & 31)) & 1u ? v[c] : -INFINITY;
-          }
-          float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int c = 4; c < 64; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], v[c], v[c + 1]);
-          const float tmax = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-          // Moves the row maximum when it grew by more than 2^kGrow (and, with
-          // the tile's first half, the value scale): rescales l, the O row and,
-          // for the second half, the first half's P
-          const bool grow_m = tmax > m_used + kGrow;
-          if (__any_sync(0xffffffffu, grow_m) || fv != 1.f) {
-            float corr = 1.f;
-            if (grow_m) {
-              corr = ex2_approx(m_used - tmax);  // 0 when m_used is -inf
-              m_used = tmax;
-              l *= corr;
-            }
-            const float fo = corr * fv;
-            fv = 1.f;
-            if (t > 0) {
-              ok = mbar_wait_warp(&pv_done[q], (uint32_t)(t - 1) & 1u, abort_flag);
-              if (ok) {
-                tc_fence_after();
-#pragma unroll 1
-                for (int c0 = 0; c0 < DH; c0 += 16) {
-                  float o16[16];
-                  tmem_ld16(tO + (uint32_t)c0, o16);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o16[e] *= fo;
-                  tmem_st16(tO + (uint32_t)c0, o16);
-                }
-              }
-            }
-            if (hf == 1) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < 32; c0 += 16) {
-                float w16[16];
-                tmem_ld16(tS + (uint32_t)c0, w16);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w16[e]));
-                  const __half2 h2 = __floats2half2_rn(f.x * corr, f.y * corr);
-                  w16[e] = *reinterpret_cast<const float*>(&h2);
-                }
-                tmem_st16(tS + (uint32_t)c0, w16);
-              }
-            }
-          }
-          const float moff = (m_used == -INFINITY) ? 0.f : m_used;
+        const float* sc = sScale + (t & 3) * BK;
+        const float fv = sGrow[t & 3];  // growth of the value scale
+        // scores relative to the row maximum, base 2
+        float x[128];
+        tc_fence_after();
+        tmem_ld128(tS, x);
+        const float moff = m_used == -INFINITY ? 0.f : m_used;
+        {
           const unsigned long long m2 = f2_pack(-moff, -moff);
-          const ulonglong2* v2 = reinterpret_cast<const ulonglong2*>(sc + BK + hf * 64);
-          uint32_t pk[32];
-          unsigned long long sum2[4] = {0ull, 0ull, 0ull, 0ull};
-          auto weights = [&](auto is_masked) {
+          const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(sc);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const ulonglong2 k = k2[c];
+            f2_unpack(f2_fma(f2_pack(x[4 * c], x[4 * c + 1]), k.x, m2), x[4 * c], x[4 * c + 1]);
+            f2_unpack(f2_fma(f2_pack(x[4 * c + 2], x[4 * c + 3]), k.y, m2), x[4 * c + 2], x[4 * c + 3]);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t m = row_mask(tile * BK + h * 32, Lb, node, depth, p);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[h * 32 + c] = (m >> c) & 1u ? x[h * 32 + c] : -INFINITY;
+          }
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < 128; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+        const float tmax = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+        // Moves the row maximum when it grew by more than 2^kGrow (or the row
+        // met its first key), and follows the value scale: rescales l and O
+        const bool grow_m = tmax > kGrow || (m_used == -INFINITY && tmax != -INFINITY);
+        if (__any_sync(0xffffffffu, grow_m) || fv != 1.f) {
+          float corr = 1.f, d = 0.f;
+          if (grow_m) {
+            d = -tmax;
+            corr = m_used == -INFINITY ? 0.f : ex2_approx(d);
+            m_used = moff + tmax;
+            l *= corr;
+          }
+          const float fo = corr * fv;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] += d;
+          if (t > 0) {
+            ok = mbar_wait_warp(&pv_done[q], (uint32_t)(t - 1) & 1u, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < DH; c0 += 8) {
+              float o8[8];
+              tmem_ld8(tO + (uint32_t)c0, o8);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o8[e] *= fo;
+              tmem_st8(tO + (uint32_t)c0, o8);
+            }
+          }
+        }
+        // weights x 2^7, as fp16 pairs over the S columns just read; a masked
+        // tile takes every exponential on MUFU, which gives exactly 0 there
+        unsigned long long sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        auto weights = [&](auto is_masked) {
+          const unsigned long long seven = f2_pack(7.f, 7.f);
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const ulonglong2 s2 = v2[c];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c2 = 2 * c + h;
-                float x0, x1, e0, e1;
-                f2_unpack(f2_add(f2_pack(v[2 * c2], v[2 * c2 + 1]), m2), x0, x1);
-                if (!decltype(is_masked)::value && (c2 & 3) == 3) {
-                  exp2_fma2(x0, x1, e0, e1);  // one pair in four on the FMA pipe
-                } else {
-                  e0 = ex2_approx(x0);
-                  e1 = ex2_approx(x1);
-                }
-                const unsigned long long e2 = f2_pack(e0, e1);
-                sum2[c2 & 3] = f2_add(sum2[c2 & 3], e2);
-                float p0, p1;
-                f2_unpack(f2_mul(e2, h ? s2.y : s2.x), p0, p1);
-                if constexpr (decltype(is_masked)::value) {
-                  // 0, not 0 * NaN, for keys the row does not see
-                  const uint32_t mm = c2 < 16 ? m0 : m1;
-                  p0 = (mm >> ((2 * c2) & 31)) & 1u ? p0 : 0.f;
-                  p1 = (mm >> ((2 * c2 + 1) & 31)) & 1u ? p1 : 0.f;
-                }
-                const __half2 hh = __floats2half2_rn(p0, p1);
-                pk[c2] = *reinterpret_cast<const uint32_t*>(&hh);
+              const int c2 = c0 + c;
+              float x0, x1, e0, e1;
+              f2_unpack(f2_add(f2_pack(x[2 * c2], x[2 * c2 + 1]), seven), x0, x1);
+              if (!decltype(is_masked)::value && (c2 & 3) == 3) {
+                exp2_fma2(x0, x1, e0, e1);  // one pair in four on the FMA pipe
+              } else {
+                e0 = ex2_approx(x0);
+                e1 = ex2_approx(x1);
               }
+              sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
+              const __half2 hh = __floats2half2_rn(e0, e1);
+              pk[c] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-          };
-          if (masked) weights(std::true_type{});
-          else weights(std::false_type{});
-          float a0, a1, b0, b1, c0, c1, d0, d1;
-          f2_unpack(sum2[0], a0, a1);
-          f2_unpack(sum2[1], b0, b1);
-          f2_unpack(sum2[2], c0, c1);
-          f2_unpack(sum2[3], d0, d1);
-          l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
-          tmem_st32(tS + (uint32_t)(hf * 64), pk);  // P over the S columns just read
-        }
-        if (!ok) break;
+            tmem_st16_nowait(tS + (uint32_t)c0, pk);
+          }
+          tmem_wait_st();
+        };
+        if (masked) weights(std::true_type{});
+        else weights(std::false_type{});
+        float a0, a1, b0, b1, c0, c1, d0, d1;
+        f2_unpack(sum2[0], a0, a1);
+        f2_unpack(sum2[1], b0, b1);
+        f2_unpack(sum2[2], c0, c1);
+        f2_unpack(sum2[3], d0, d1);
+        l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
       }
       tc_fence_before();
       __syncwarp();
@@ -513,8 +523,9 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       ok = mbar_wait_warp(&pv_done[q], (uint32_t)(T - 1) & 1u, abort_flag);
       if (ok) {
         tc_fence_after();
-        const float vref = sRef[(T - 1) & 3];
-        const float f = p.P == 1 ? (l == 0.f ? 0.f : vref / l) : vref;
+        // weights and l carry 2^7, V 2^10 / vref
+        const float vref = sRef[(T - 1) & 3] * 0x1p-10f;
+        const float f = p.P == 1 ? (l == 0.f ? 0.f : vref / l) : vref * 0x1p-7f;
         const int g = grow_ - node * p.G;
         __nv_bfloat16* ob =
             p.out + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH;
@@ -528,7 +539,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int jj = (e >> 1) & 3;
-            d[(e & 8) + jj + 4 * (e & 1)] = o16[e] * ((jj & 1) ? 0x1p13f : 0x1p17f) * f;
+            d[(e & 8) + jj + 4 * (e & 1)] = o16[e] * f;
           }
           if (p.P == 1) {
             __align__(16) __nv_bfloat162 h[8];
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
           }
         }
         // (a sum of NaN must reach the merge, which skips m = -inf)
-        if (p.P > 1 && row_ok) p.pml[prow] = make_float2(l != l && m_used == -INFINITY ? 0.f : m_used, l);
+        if (p.P > 1 && row_ok) p.pml[prow] = make_float2(l != l && m_used == -INFINITY ? 0.f : m_used, l * 0x1p-7f);
       }
     }
   }

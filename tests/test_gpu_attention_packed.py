@@ -39,10 +39,13 @@ def _values(c):
     return R.decode(c.k_codes, c.k_par), R.decode(c.v_codes, c.v_par)
 
 
-def _weights(dtype, dh, G=1, packed=True):
+def _weights(dtype, dh, G, N, packed=True):
+    """Rounding of the kernel that takes this shape (ext_reference.C_P)."""
     if dtype == F32 or dh == 64 or (not packed and 128 % G):
         return "fp32"
-    return "fp16" if packed else "bf16"
+    if not packed:
+        return "bf16"
+    return "fp16v" if N * G > 128 else "fp16"
 
 
 # (B, tree (K, s, N), Hq, Hkv, dh, prefix lengths, dtype)
@@ -74,7 +77,7 @@ def test_packed_matches_the_formula(B, tree, Hq, Hkv, dh, Ls, dtype, window, sin
     scale = 1 / math.sqrt(dh)
     got = api.medusa_tree_attention_packed(q, c, L, api.Tree(*tree), scale, window, sinks)
     ref = R.attention(q, *_values(c), Ls, O.tree_plan(*tree), scale, window, sinks)
-    R.assert_close(got, *ref, dtype, _weights(dtype, dh))
+    R.assert_close(got, *ref, dtype, _weights(dtype, dh, Hq // Hkv, tree[2]))
     assert api.device_status() == 0
 
 
@@ -93,16 +96,17 @@ def test_window_matches_the_formula(B, tree, Hq, Hkv, dh, Ls, dtype, window, sin
     got = api.medusa_tree_attention_window(q, k, v, L, t, scale, window, sinks)
     ref = R.attention(q, k.double().transpose(1, 2), v.double().transpose(1, 2), Ls,
                       O.tree_plan(*tree), scale, window, sinks)
-    R.assert_close(got, *ref, dtype, _weights(dtype, dh, Hq // Hkv, packed=False))
+    R.assert_close(got, *ref, dtype, _weights(dtype, dh, Hq // Hkv, N, packed=False))
     assert api.device_status() == 0
 
 
+@pytest.mark.parametrize("tree,Hq", [((5, 10, 64), 2), ((1, 1, 1), 8), ((4, 3, 5), 6),
+                                     ((4, 3, 9), 6), ((5, 10, 50), 4), ((5, 3, 200), 2)])
 @pytest.mark.parametrize("scale_q", [1e-3, 40.0])
-def test_packed_growing_maxima(scale_q):
+def test_packed_growing_maxima(scale_q, tree, Hq):
     """Scores that grow along the prefix (the running maximum moves in every
-    tile) and value scales that grow by 2^40 over it."""
-    tree = (5, 10, 64)
-    q, c, L, Lcap = _packed_inputs(1, tree, 2, 2, 128, [1500], BF, spare=0)
+    tile) and value scales that grow by 2^40 over it, in every kernel."""
+    q, c, L, Lcap = _packed_inputs(1, tree, Hq, 2, 128, [1500], BF, spare=0)
     q = (q.float() * scale_q).to(BF)
     ramp = torch.linspace(0, 1, Lcap, device=DEV)
     c.k_par[..., 0] *= (1 + 6 * ramp).to(BF)
@@ -111,7 +115,7 @@ def test_packed_growing_maxima(scale_q):
     for w, s in ((0, 0), (300, 7)):
         got = api.medusa_tree_attention_packed(q, c, L, api.Tree(*tree), scale, w, s)
         ref = R.attention(q, *_values(c), [1500], O.tree_plan(*tree), scale, w, s)
-        R.assert_close(got, *ref, BF, "fp16")
+        R.assert_close(got, *ref, BF, _weights(BF, 128, Hq // 2, tree[2]))
 
 
 @pytest.mark.parametrize("B,tree,Hq,Hkv,dh,Ls,dtype", [SHAPES[2], SHAPES[4], SHAPES[6], SHAPES[8],
@@ -139,9 +143,11 @@ def test_slots_no_node_sees_may_hold_anything(B, tree, Hq, Hkv, dh, Ls, dtype, w
     assert torch.equal(api.medusa_tree_attention_window(q, k, v, L, t, scale, window, sinks), cleanw)
 
 
-@pytest.mark.parametrize("dh,dtype", [(128, BF), (64, BF), (128, F32)])
-def test_a_visible_nan_row_reaches_exactly_its_nodes(dh, dtype):
-    tree, Ls = (4, 3, 16), [70, 200]
+@pytest.mark.parametrize("dh,dtype,tree", [(128, BF, (4, 3, 16)), (64, BF, (4, 3, 16)),
+                                           (128, F32, (4, 3, 16)), (128, BF, (4, 3, 6)),
+                                           (128, BF, (4, 3, 60)), (128, BF, (5, 3, 110))])
+def test_a_visible_nan_row_reaches_exactly_its_nodes(dh, dtype, tree):
+    Ls = [70, 200]
     q, c, L, _ = _packed_inputs(2, tree, 4, 2, dh, Ls, dtype)
     depth, anc = R.tree_masks(O.tree_plan(*tree))
     c.k_par[0, 1, 70 + 3] = math.nan         # node 3's key of kv-head 1
@@ -179,7 +185,7 @@ def test_sequences_that_do_not_fit_and_canaries(dtype, dh):
                 assert out.t[1].abs().max() == 0
                 ref = R.attention(q, *(_values(c) if packed else (x.double().transpose(1, 2) for x in (k, v))),
                                   [100, bad, 40], O.tree_plan(*tree), scale, w, s)
-                R.assert_close(out.t, *ref, dtype, _weights(dtype, dh, Hq // Hkv, packed))
+                R.assert_close(out.t, *ref, dtype, _weights(dtype, dh, Hq // Hkv, tree[2], packed))
 
 
 def test_unwindowed_call_equals_tree_attention():
