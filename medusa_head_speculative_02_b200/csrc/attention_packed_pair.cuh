@@ -2,7 +2,7 @@
 // than 128): two 128-row query tiles per CTA, query rows as the MMAs' rows.
 // Included by attention_packed_tc.cu.
 //
-// Same arithmetic as tree_attn_packed_kernel.  With this many rows the
+// With this many rows the
 // products bound the call, not the cache, and a tile's work per softmax
 // thread decides: a thread here owns one query row and all 128 keys of a
 // tile, keeps the row's maximum and sum to itself (no votes, no weights
@@ -14,9 +14,12 @@
 //   O += P V    A = P from TMEM (fp16), B = V MN-major
 // Both tiles read every unpacked K/V tile.  MMA order S_a(0), S_b(0), then
 // PV_a(t), S_a(t+1), PV_b(t), S_b(t+1): one tile's products run during the
-// other's softmax.  The unpack warps write the scales of a tile beside it:
-// sk * softmax scale, and sv relative to a power of two >= the largest sv so
-// far times 2^-7, whose growth (a factor they pass on) rescales O.
+// other's softmax.  K and V are unpacked with their scales, relative to a power
+// of two >= the tile's largest for K (one factor on the tile's scores) and >=
+// the largest so far for V (its growth rescales O), and rounded once to fp16:
+// scales read from shared memory by every softmax thread (128 a tile) made the
+// call 1.25 x as long.  A row whose K or V has no finite scale is stored as 0
+// and put back as NaN scores, so that it reaches the rows that see it only.
 // Warpgroups: 0 TMA (ring of K and V code tiles) and MMA issue, 1 unpack, 2
 // and 3 the softmax of query tiles a and b.
 
@@ -30,8 +33,7 @@ struct PairCfg {
   static constexpr uint32_t oK = 2 * kTile;
   static constexpr uint32_t oV = oK + 2 * kTile;
   static constexpr uint32_t oRing = oV + 2 * kTile;
-  static constexpr uint32_t oScale = oRing + kItems * kItem;
-  static constexpr uint32_t oMisc = oScale + 4 * BK * 4;
+  static constexpr uint32_t oMisc = oRing + kItems * kItem;
   static constexpr size_t kSmem = 1024 + oMisc + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -51,6 +53,35 @@ __device__ __forceinline__ void unpack_word_scaled(uint32_t w, __half2 z1, __hal
                               (j & 1) ? a16 : a1);
     r[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
+}
+
+// 2^(q2 x s + m2) for the 64 scores of one key half as fp16 pairs (pk[c]: keys
+// 2c, 2c + 1); returns their fp32 sum.  One pair in four on the FMA pipe
+// unless the half holds masked (-inf) scores, where MUFU's exact 0 is needed.
+template <bool kMasked>
+__device__ __forceinline__ float exp_pack64_f16(const float (&v)[64], unsigned long long q2,
+                                                unsigned long long m2, uint32_t (&pk)[32]) {
+  unsigned long long sum2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int c2 = 0; c2 < 32; ++c2) {
+    float x0, x1, e0, e1;
+    f2_unpack(f2_fma(f2_pack(v[2 * c2], v[2 * c2 + 1]), q2, m2), x0, x1);
+    if (!kMasked && (c2 & 3) == 3) {
+      exp2_fma2(x0, x1, e0, e1);
+    } else {
+      e0 = ex2_approx(x0);
+      e1 = ex2_approx(x1);
+    }
+    sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
+    const __half2 h2 = __floats2half2_rn(e0, e1);
+    pk[c2] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  float a0, a1, b0, b1, c0f, c1f, d0, d1;
+  f2_unpack(sum2[0], a0, a1);
+  f2_unpack(sum2[1], b0, b1);
+  f2_unpack(sum2[2], c0f, c1f);
+  f2_unpack(sum2[3], d0, d1);
+  return ((a0 + a1) + (b0 + b1)) + ((c0f + c1f) + (d0 + d1));
 }
 
 // Visible keys of the 32 slots from s0 for a query row (node, depth): prefix
@@ -89,6 +120,12 @@ __device__ __forceinline__ uint32_t row_mask(int s0, int Lb, int node, int depth
   return m;
 }
 
+// The power of two >= a scale (its bits), kept in [2^-120, 2^119].
+__device__ __forceinline__ float scale_ref(uint32_t bits) {
+  const int ex = min(246, max(7, (int)((bits >> 23) + ((bits & 0x7fffffu) ? 1 : 0))));
+  return __uint_as_float((uint32_t)ex << 23);
+}
+
 __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     tree_attn_packed_pair_kernel(const __grid_constant__ CUtensorMap tmKc,
                                  const __grid_constant__ CUtensorMap tmVc,
@@ -102,7 +139,6 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
   uint8_t* sK = sm + C::oK;
   uint8_t* sV = sm + C::oV;
   uint8_t* sRing = sm + C::oRing;
-  float* sScale = (float*)(sm + C::oScale);  // [4][128]: K scale x softmax scale
   uint64_t* it_full = (uint64_t*)(sm + C::oMisc);  // [kItems]
   uint64_t* it_empty = it_full + C::kItems;  // [kItems]
   uint64_t* k_ready = it_empty + C::kItems;  // [2]
@@ -118,8 +154,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
   unsigned* qmax = (unsigned*)(tmem_slot + 2);
   float* sGrow = (float*)(tmem_slot + 4);  // [4] factor on O before the tile
   float* sRef = sGrow + 4;                 // [4] power of two of the value scales
-  unsigned* sMax = (unsigned*)(sRef + 4);  // [2][4] largest value scale of the unpack warps
-  static_assert((2 * C::kItems + 15) * 8 + 16 + 32 + 32 <= 512, "barrier block");
+  float* sScore = sRef + 4;                // [4] scale of the scores
+  unsigned* sNan = (unsigned*)(sScore + 4);  // [4][4] keys in use without a finite scale
+  unsigned* sMax = sNan + 16;                // [2][K 4 | V 4] largest scales of the unpack warps
+  static_assert((2 * C::kItems + 15) * 8 + 16 + 48 + 64 + 64 <= 512, "barrier block");
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -215,7 +253,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     const float f[4] = {bf16_lo(qv[i].x), bf16_hi(qv[i].x), bf16_lo(qv[i].y), bf16_hi(qv[i].y)};
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
-      dst[2 * jj + h] = __float2half_rn(f[jj] * ((jj & 1) ? qs * 0.0625f : qs));
+      dst[2 * jj + h] = __float2half_rn(f[jj] * qs);
   }
   fence_proxy_async_smem();
   __syncthreads();
@@ -287,7 +325,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         const uint32_t tOq = tmem + 256u + (uint32_t)q * 128u;
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16_ts_warp(tOq, aP + (uint32_t)(kk * 8),
+          umma_f16_ts_warp(tOq, aP + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8),
                            dv + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
                            (u > 0 || kk > 0) ? 1u : 0u);
         if (q == 1) umma_commit_warp(&v_empty[st]);  // both tiles have read V(u)
@@ -308,10 +346,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     // ---------------------------------------------------------------- unpack
     reg_dec<C::kRegsUnpack>();
     const int sw = (key >> 1) & 3;  // 64-byte swizzle of the code rows
-    const float cscale = p.scale2 * ldexpf(1.f, 24 - kexp);
     float vref = 0x1p-120f;
     bool ok = true;
-    uint32_t vp = 0u;
+    uint32_t kp = 0u, vp = 0u;
+    float kref = 0.f;
     for (int i = 0; i < 2 * T && ok; ++i) {
       const int t = i >> 1, st = i % C::kItems, bf = t & 1;
       const bool isV = i & 1;
@@ -324,49 +362,50 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         }
       } else {
         const uint32_t* par = (const uint32_t*)(sRing + st * C::kItem + kCodeTile);
+        kp = par[key];
         vp = par[BK + key];
-        // the largest value scale of the keys in use; every warp of the group
-        // takes part (an error ends them together)
+        // the largest scales of the keys in use; every warp of the group takes
+        // part (an error ends them together)
         const int slot = tl.tile(j0 + t) * BK + key;
         const bool live = slot < Lb + p.N && in_window(slot, Lb, p.window, p.sinks);
+        const uint32_t ak = __float_as_uint(fabsf(bf16_lo(kp)));
         const uint32_t av = __float_as_uint(fabsf(bf16_lo(vp)));
-        const unsigned sb = __reduce_max_sync(0xffffffffu, live && av < 0x7f800000u ? av : 0u);
-        if (lane == 0) sMax[bf * 4 + qd] = sb;
+        const bool fin = ak < 0x7f800000u && av < 0x7f800000u;
+        const unsigned mk = __reduce_max_sync(0xffffffffu, live && fin ? ak : 0u);
+        const unsigned mv = __reduce_max_sync(0xffffffffu, live && fin ? av : 0u);
+        const unsigned nan = __ballot_sync(0xffffffffu, live && !fin);
+        if (lane == 0) {
+          sMax[bf * 8 + qd] = mk;
+          sMax[bf * 8 + 4 + qd] = mv;
+        }
         if (bar_red_or(1, 128, !ok)) break;
-        const unsigned bb = max(max(sMax[bf * 4], sMax[bf * 4 + 1]), max(sMax[bf * 4 + 2], sMax[bf * 4 + 3]));
-        // power of two >= the largest scale, kept in [2^-120, 2^119]
-        const int ex = min(246, max(7, (int)((bb >> 23) + ((bb & 0x7fffffu) ? 1 : 0))));
-        const float nref = fmaxf(vref, __uint_as_float((uint32_t)ex << 23));
+        const unsigned* sx = sMax + bf * 8;
+        const float nk = scale_ref(max(max(sx[0], sx[1]), max(sx[2], sx[3])));
+        const float nref = fmaxf(vref, scale_ref(max(max(sx[4], sx[5]), max(sx[6], sx[7]))));
         const float grow = vref / nref;
+        kref = nk;
         vref = nref;
         if (t >= 2) ok = mbar_wait_warp(&k_empty[bf], prev, abort_flag);
-        // softmax(t - 4) has read this scale buffer: S(t - 2) followed its P(t - 3)
-        // (a V row with no finite scale is stored as 0 and shows in the scores instead,
-        // so that it reaches the rows that see it and no other)
-        sScale[(t & 3) * BK + key] =
-            fabsf(bf16_lo(vp)) <= 3.3895314e38f ? bf16_lo(par[key]) * cscale : NAN;
+        // softmax(t - 4) has read these slots: S(t - 2) followed its P(t - 3)
+        if (lane == 0) sNan[(t & 3) * 4 + qd] = nan;
         if (key == 0) {
+          // Q carries 2^kexp, K 2^10 / kref
+          sScore[t & 3] = p.scale2 * ldexpf(1.f, -kexp) * (kref * 0x1p-10f);
           sGrow[t & 3] = grow;
           sRef[t & 3] = vref;
         }
       }
       uint32_t w[16];
       const uint8_t* row = sRing + st * C::kItem + key * 64;
-      __half2 z24, z20;
-      __half2 a1, a16;
-      if (isV) {
-        const float z = fminf(fmaxf(bf16_hi(vp), 0.f), 15.f);
-        z24 = __float2half2_rn(-1024.f - z);
-        z20 = __float2half2_rn(-1024.f - 16.f * z);
-        // sv 2^10 / vref; none for a scale that is not finite or larger than
-        // those in use (a slot that no row sees)
-        float sv = bf16_lo(vp);
-        sv = fabsf(sv) <= vref ? sv * __uint_as_float((264u << 23) - __float_as_uint(vref)) : 0.f;
-        a1 = __float2half2_rn(sv);
-        a16 = __float2half2_rn(sv * 0.0625f);
-      } else {
-        zero_pairs(((const uint32_t*)(sRing + st * C::kItem + kCodeTile))[key], z24, z20);
-      }
+      // scale 2^10 / ref; none for a scale that is not finite or larger than
+      // those in use (a slot that no row sees)
+      const uint32_t par = isV ? vp : kp;
+      const float ref = isV ? vref : kref;
+      const float z = fminf(fmaxf(bf16_hi(par), 0.f), 15.f);
+      float sc = bf16_lo(par);
+      sc = fabsf(sc) <= ref ? sc * __uint_as_float((264u << 23) - __float_as_uint(ref)) : 0.f;
+      const __half2 z1 = __float2half2_rn(-1024.f - z), z16 = __float2half2_rn(-1024.f - 16.f * z);
+      const __half2 a1 = __float2half2_rn(sc), a16 = __float2half2_rn(sc * 0.0625f);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<uint4*>(&w[4 * e]) = *reinterpret_cast<const uint4*>(row + ((e ^ sw) << 4));
@@ -378,8 +417,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           uint32_t r[4];
-          if (isV) unpack_word_scaled(w[e], z24, z20, a1, a16, r);
-          else unpack_word(w[e], z24, z20, r);
+          unpack_word_scaled(w[e], z1, z16, a1, a16, r);
           *reinterpret_cast<uint4*>(dst + (e >> 3) * kAtom + (((e & 7) ^ (key & 7)) << 4)) =
               make_uint4(r[0], r[1], r[2], r[3]);
         }
@@ -422,98 +460,83 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       if (live) {
         const int tile = tl.tile(j0 + t);
         const bool masked = tile >= m_hi || tile <= m_lo;
-        const float* sc = sScale + (t & 3) * BK;
-        const float fv = sGrow[t & 3];  // growth of the value scale
-        // scores relative to the row maximum, base 2
-        float x[128];
-        tc_fence_after();
-        tmem_ld128(tS, x);
-        const float moff = m_used == -INFINITY ? 0.f : m_used;
-        {
-          const unsigned long long m2 = f2_pack(-moff, -moff);
-          const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(sc);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const ulonglong2 k = k2[c];
-            f2_unpack(f2_fma(f2_pack(x[4 * c], x[4 * c + 1]), k.x, m2), x[4 * c], x[4 * c + 1]);
-            f2_unpack(f2_fma(f2_pack(x[4 * c + 2], x[4 * c + 3]), k.y, m2), x[4 * c + 2], x[4 * c + 3]);
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t m = row_mask(tile * BK + h * 32, Lb, node, depth, p);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) x[h * 32 + c] = (m >> c) & 1u ? x[h * 32 + c] : -INFINITY;
-          }
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int c = 4; c < 128; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
-        const float tmax = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-        // Moves the row maximum when it grew by more than 2^kGrow (or the row
-        // met its first key), and follows the value scale: rescales l and O
-        const bool grow_m = tmax > kGrow || (m_used == -INFINITY && tmax != -INFINITY);
-        if (__any_sync(0xffffffffu, grow_m) || fv != 1.f) {
-          float corr = 1.f, d = 0.f;
-          if (grow_m) {
-            d = -tmax;
-            corr = m_used == -INFINITY ? 0.f : ex2_approx(d);
-            m_used = moff + tmax;
-            l *= corr;
-          }
-          const float fo = corr * fv;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] += d;
-          if (t > 0) {
-            ok = mbar_wait_warp(&pv_done[q], (uint32_t)(t - 1) & 1u, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
+        const uint32_t* nk = sNan + (t & 3) * 4;
+        const bool bad_key = (nk[0] | nk[1] | nk[2] | nk[3]) != 0u;  // (rare) rows without a scale
+        const float sf = sScore[t & 3];  // scores of this tile: S x sf, base 2
+        float fv = sGrow[t & 3];         // growth of the value scale, once per tile
+        const unsigned long long q2 = f2_pack(sf, sf);
 #pragma unroll 1
-            for (int c0 = 0; c0 < DH; c0 += 8) {
-              float o8[8];
-              tmem_ld8(tO + (uint32_t)c0, o8);
+        for (int hf = 0; hf < 2; ++hf) {
+          float v[64];
+          tc_fence_after();
+          tmem_ld64(tS + (uint32_t)(hf * 64), v);
+          if (masked || bad_key) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o8[e] *= fo;
-              tmem_st8(tO + (uint32_t)c0, o8);
-            }
-          }
-        }
-        // weights x 2^7, as fp16 pairs over the S columns just read; a masked
-        // tile takes every exponential on MUFU, which gives exactly 0 there
-        unsigned long long sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        auto weights = [&](auto is_masked) {
-          const unsigned long long seven = f2_pack(7.f, 7.f);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t m = row_mask(tile * BK + hf * 64 + h * 32, Lb, node, depth, p);
+              const uint32_t nan = sNan[(t & 3) * 4 + hf * 2 + h];
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const int c2 = c0 + c;
-              float x0, x1, e0, e1;
-              f2_unpack(f2_add(f2_pack(x[2 * c2], x[2 * c2 + 1]), seven), x0, x1);
-              if (!decltype(is_masked)::value && (c2 & 3) == 3) {
-                exp2_fma2(x0, x1, e0, e1);  // one pair in four on the FMA pipe
-              } else {
-                e0 = ex2_approx(x0);
-                e1 = ex2_approx(x1);
+              for (int c = 0; c < 32; ++c) {
+                const float x = (nan >> c) & 1u ? NAN : v[h * 32 + c];
+                v[h * 32 + c] = (m >> c) & 1u ? x : -INFINITY;
               }
-              sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
-              const __half2 hh = __floats2half2_rn(e0, e1);
-              pk[c] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            tmem_st16_nowait(tS + (uint32_t)c0, pk);
           }
-          tmem_wait_st();
-        };
-        if (masked) weights(std::true_type{});
-        else weights(std::false_type{});
-        float a0, a1, b0, b1, c0, c1, d0, d1;
-        f2_unpack(sum2[0], a0, a1);
-        f2_unpack(sum2[1], b0, b1);
-        f2_unpack(sum2[2], c0, c1);
-        f2_unpack(sum2[3], d0, d1);
-        l += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
+          float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int c = 4; c < 64; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], v[c], v[c + 1]);
+          const float tmax = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sf;
+          // Moves the row maximum when it grew by more than 2^kGrow (and, with
+          // the tile's first half, follows the value scale): rescales l, the O
+          // row and, for the second half, the first half's P
+          const bool grow_m = tmax > m_used + kGrow;
+          if (__any_sync(0xffffffffu, grow_m) || fv != 1.f) {
+            float corr = 1.f;
+            if (grow_m) {
+              corr = ex2_approx(m_used - tmax);  // 0 when m_used is -inf
+              m_used = tmax;
+              l *= corr;
+            }
+            const float fo = corr * fv;
+            fv = 1.f;
+            if (t > 0) {
+              ok = mbar_wait_warp(&pv_done[q], (uint32_t)(t - 1) & 1u, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < DH; c0 += 16) {
+                float o16[16];
+                tmem_ld16(tO + (uint32_t)c0, o16);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o16[e] *= fo;
+                tmem_st16(tO + (uint32_t)c0, o16);
+              }
+            }
+            if (hf == 1) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < 32; c0 += 16) {
+                float w16[16];
+                tmem_ld16(tS + (uint32_t)c0, w16);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w16[e]));
+                  const __half2 h2 = __floats2half2_rn(f.x * corr, f.y * corr);
+                  w16[e] = *reinterpret_cast<const float*>(&h2);
+                }
+                tmem_st16(tS + (uint32_t)c0, w16);
+              }
+            }
+          }
+          // weights x 2^7 as fp16 pairs over the S columns just read; a masked
+          // tile takes every exponential on MUFU, which gives exactly 0 there
+          const float moff = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
+          const unsigned long long m2 = f2_pack(-moff, -moff);
+          uint32_t pk[32];
+          l += masked || bad_key ? exp_pack64_f16<true>(v, q2, m2, pk)
+                                 : exp_pack64_f16<false>(v, q2, m2, pk);
+          tmem_st32(tS + (uint32_t)(hf * 64), pk);
+        }
+        if (!ok) break;
       }
       tc_fence_before();
       __syncwarp();
