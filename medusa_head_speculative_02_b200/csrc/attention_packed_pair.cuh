@@ -56,9 +56,9 @@ __device__ __forceinline__ void unpack_word_scaled(uint32_t w, __half2 z1, __hal
 }
 
 // 2^(q2 x s + m2) for the 64 scores of one key half as fp16 pairs (pk[c]: keys
-// 2c, 2c + 1); returns their fp32 sum.  One pair in four on the FMA pipe
-// unless the half holds masked (-inf) scores, where MUFU's exact 0 is needed.
-template <bool kMasked>
+// 2c, 2c + 1); returns their fp32 sum.  Every exponential on MUFU (one pair in
+// two, four or eight by polynomial on the FMA pipe: 132, 124 and 120 us against
+// 119 at the 8B-GQA shape, 4 sequences).
 __device__ __forceinline__ float exp_pack64_f16(const float (&v)[64], unsigned long long q2,
                                                 unsigned long long m2, uint32_t (&pk)[32]) {
   unsigned long long sum2[4] = {0ull, 0ull, 0ull, 0ull};
@@ -66,12 +66,8 @@ __device__ __forceinline__ float exp_pack64_f16(const float (&v)[64], unsigned l
   for (int c2 = 0; c2 < 32; ++c2) {
     float x0, x1, e0, e1;
     f2_unpack(f2_fma(f2_pack(v[2 * c2], v[2 * c2 + 1]), q2, m2), x0, x1);
-    if (!kMasked && (c2 & 3) == 3) {
-      exp2_fma2(x0, x1, e0, e1);
-    } else {
-      e0 = ex2_approx(x0);
-      e1 = ex2_approx(x1);
-    }
+    e0 = ex2_approx(x0);
+    e1 = ex2_approx(x1);
     sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
     const __half2 h2 = __floats2half2_rn(e0, e1);
     pk[c2] = *reinterpret_cast<const uint32_t*>(&h2);
@@ -207,6 +203,26 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     }
     return;
   }
+  // the first code tiles are under way while Q is prepared
+  const uint64_t pol = policy_evict_normal();
+  auto load_item = [&](int i) {
+    const int st = i % C::kItems;
+    const int key0 = tl.tile(j0 + (i >> 1)) * BK;
+    dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
+    uint8_t* dst = sRing + st * C::kItem;
+    if (i & 1) {
+      mbar_arrive_expect_tx(&it_full[st], kCodeTile);
+      tma_load_3d(dst, &tmVc, &it_full[st], 0, key0, bk, pol);
+    } else {
+      mbar_arrive_expect_tx(&it_full[st], C::kItem);
+      tma_load_3d(dst, &tmKc, &it_full[st], 0, key0, bk, pol);
+      tma_load_2d(dst + kCodeTile, &tmKp, &it_full[st], key0, bk, pol);
+      tma_load_2d(dst + kCodeTile + BK * 4, &tmVp, &it_full[st], key0, bk, pol);
+    }
+  };
+  const int early = min(2 * T, C::kItems);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < early; ++i) load_item(i);
   __syncthreads();  // qmax
   // Q as fp16 under one power of two, dims in the unpacked codes' order (as in
   // tree_attn_packed_kernel): 16 rows per warp
@@ -265,23 +281,11 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     reg_dec<C::kRegs0>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- TMA producer
-      const uint64_t pol = policy_evict_normal();
-      int issued = 0;
-      for (int i = 0; i < 2 * T; ++i) {
+      int issued = early;
+      for (int i = early; i < 2 * T; ++i) {
         const int st = i % C::kItems;
-        const int key0 = tl.tile(j0 + (i >> 1)) * BK;
-        dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
         if (!mbar_wait(&it_empty[st], ((uint32_t)(i / C::kItems) & 1u) ^ 1u, abort_flag)) break;
-        uint8_t* dst = sRing + st * C::kItem;
-        if (i & 1) {
-          mbar_arrive_expect_tx(&it_full[st], kCodeTile);
-          tma_load_3d(dst, &tmVc, &it_full[st], 0, key0, bk, pol);
-        } else {
-          mbar_arrive_expect_tx(&it_full[st], C::kItem);
-          tma_load_3d(dst, &tmKc, &it_full[st], 0, key0, bk, pol);
-          tma_load_2d(dst + kCodeTile, &tmKp, &it_full[st], key0, bk, pol);
-          tma_load_2d(dst + kCodeTile + BK * 4, &tmVp, &it_full[st], key0, bk, pol);
-        }
+        load_item(i);
         issued = i + 1;
       }
       if (issued < 2 * T) {
@@ -527,13 +531,11 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
               }
             }
           }
-          // weights x 2^7 as fp16 pairs over the S columns just read; a masked
-          // tile takes every exponential on MUFU, which gives exactly 0 there
+          // weights x 2^7 as fp16 pairs over the S columns just read
           const float moff = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
           const unsigned long long m2 = f2_pack(-moff, -moff);
           uint32_t pk[32];
-          l += masked || bad_key ? exp_pack64_f16<true>(v, q2, m2, pk)
-                                 : exp_pack64_f16<false>(v, q2, m2, pk);
+          l += exp_pack64_f16(v, q2, m2, pk);
           tmem_st32(tS + (uint32_t)(hf * 64), pk);
         }
         if (!ok) break;

@@ -267,6 +267,22 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     return;
   }
 
+  // the first code tiles are under way while Q is prepared
+  const uint64_t pol = policy_evict_normal();
+  auto load_tile = [&](int j) {
+    const int st = j % C::kStages;
+    const int key0 = tl.tile(j0 + j) * BK;
+    dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
+    mbar_arrive_expect_tx(&code_full[st], kStage);
+    uint8_t* dst = sCode + st * kStage;
+    tma_load_3d(dst, &tmKc, &code_full[st], 0, key0, bk, pol);
+    tma_load_2d(dst + 2 * kCodeTile, &tmKp, &code_full[st], key0, bk, pol);
+    tma_load_2d(dst + 2 * kCodeTile + BK * 4, &tmVp, &code_full[st], key0, bk, pol);
+    tma_load_3d(dst + kCodeTile, &tmVc, &code_full[st], 0, key0, bk, pol);
+  };
+  const int early = min(T, C::kStages);
+  if (threadIdx.x == 0)
+    for (int j = 0; j < early; ++j) load_tile(j);
   __syncthreads();  // qmax
   // Q: a warp per query row, a lane 4 dims; the largest |q| of the CTA's rows
   // sets one power-of-two factor (fp16 then holds every bf16 value down to
@@ -343,19 +359,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     reg_dec<C::kRegs0>();
     if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-      const uint64_t pol = policy_evict_normal();
-      int issued = 0;
-      for (int j = 0; j < T; ++j) {
+      int issued = early;
+      for (int j = early; j < T; ++j) {
         const int st = j % C::kStages;
-        const int key0 = tl.tile(j0 + j) * BK;
-        dbg_ok(key0 >= 0 && key0 < Lb + p.N && key0 < p.Lcap, DBG_ATTN_KEY_TILE);
         if (!mbar_wait(&code_empty[st], ((uint32_t)(j / C::kStages) & 1u) ^ 1u, abort_flag)) break;
-        mbar_arrive_expect_tx(&code_full[st], kStage);
-        uint8_t* dst = sCode + st * kStage;
-        tma_load_3d(dst, &tmKc, &code_full[st], 0, key0, bk, pol);
-        tma_load_2d(dst + 2 * kCodeTile, &tmKp, &code_full[st], key0, bk, pol);
-        tma_load_2d(dst + 2 * kCodeTile + BK * 4, &tmVp, &code_full[st], key0, bk, pol);
-        tma_load_3d(dst + kCodeTile, &tmVc, &code_full[st], 0, key0, bk, pol);
+        load_tile(j);
         issued = j + 1;
       }
       if (issued < T) {

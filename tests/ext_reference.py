@@ -11,9 +11,9 @@ the same average over |v|, S = max over visible j of scale * sum_d |q_d k_jd|):
   the weights rounded once (c_p: fp16 2^-11, bf16 2^-8 plus the 1.5e-4 of the
   polynomial exponential; fp32 none) move o by at most  c_p * A
   and "fp16v", the kernel of more than 128 query rows per kv-head, rounds the
-  decoded K and V to fp16 too and has the polynomial exponential: V is off by
+  decoded K and V to fp16 too: V is off by
   2^-11 of |v|, a score by 2^-11 S, in every weight of numerator and sum
-                                         (2^-10 + 1.5e-4 + 2 * 2^-11 S) * A
+                                                  (2^-10 + 2 * 2^-11 S) * A
   scores: a 128-term fp32 dot product is off by at most 128 * 2^-24 S = 2^-17 S,
   in every weight of the numerator and of the sum        2 * 2^-17 S * A
   fp32 sums, exponentials (2 ulp) and merges             2^-16 * A
@@ -33,7 +33,7 @@ import math
 
 import torch
 
-C_P = {"fp16": 2.0 ** -11, "fp16v": 2.0 ** -10 + 1.5e-4, "bf16": 2.0 ** -8 + 1.5e-4, "fp32": 0.0}
+C_P = {"fp16": 2.0 ** -11, "fp16v": 2.0 ** -10, "bf16": 2.0 ** -8 + 1.5e-4, "fp32": 0.0}
 
 
 def encode(x):
