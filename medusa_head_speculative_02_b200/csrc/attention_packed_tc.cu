@@ -427,16 +427,21 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     const int sw = (key >> 1) & 3;  // 64-byte swizzle of the code rows
     // cscale: scores are acc * 2^24 / 2^k * scale * log2(e) * sk
     const float cscale = p.scale2 * ldexpf(1.f, 24 - kexp);
-    for (int t = 0; t < T; ++t) {
-      const int st = t % C::kStages, bf = t & 1;
-      const uint32_t prev = ((uint32_t)(t >> 1) & 1u) ^ 1u;
-      if (!mbar_wait_warp(&code_full[st], (uint32_t)(t / C::kStages) & 1u, abort_flag)) break;
-      const uint8_t* row = sCode + st * kStage + key * 64;
-      const uint32_t* par = (const uint32_t*)(sCode + st * kStage + 2 * kCodeTile);
-      const uint32_t kp = par[key], vp = par[BK + key];
+    // One warpgroup for both unpacks K two tiles ahead of V: K(t) only waits
+    // for S(t - 2), V(t - 2) for PV(t - 4), so the products of one tile never
+    // wait for the softmax of the tile before it.
+    constexpr int kLag = C::kUnpackWgs == 1 ? 2 : 0;
+    bool ok = true;
+    for (int s = 0; s < T + kLag && ok; ++s) {
       uint32_t w[16];
       __half2 z24, z20;
-      if (doK) {
+      if (doK && s < T) {
+        const int st = s % C::kStages, bf = s & 1;
+        ok = mbar_wait_warp(&code_full[st], (uint32_t)(s / C::kStages) & 1u, abort_flag);
+        if (!ok) break;
+        const uint8_t* row = sCode + st * kStage + key * 64;
+        const uint32_t* par = (const uint32_t*)(sCode + st * kStage + 2 * kCodeTile);
+        const uint32_t kp = par[key], vp = par[BK + key];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(&w[4 * i]) = *reinterpret_cast<const uint4*>(row + ((i ^ sw) << 4));
@@ -444,12 +449,13 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&code_empty[st]);
         }
-        if (t >= 2) {  // S(t - 2) has read this K buffer
-          if (!mbar_wait_warp(&s_full[bf], prev, abort_flag)) break;
+        if (s >= 2) {  // S(s - 2) has read this K buffer
+          ok = mbar_wait_warp(&s_full[bf], ((uint32_t)(s >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
         }
-        // softmax(t - 4) has read this scale buffer: S(t - 2) was issued after s_free(t - 4)
-        sScale[(t & (kScaleBufs - 1)) * 2 * BK + key] = bf16_lo(kp) * cscale;
-        sScale[(t & (kScaleBufs - 1)) * 2 * BK + BK + key] = bf16_lo(vp);
+        // softmax(s - 4) has read this scale buffer: S(s - 2) was issued after s_free(s - 4)
+        sScale[(s & (kScaleBufs - 1)) * 2 * BK + key] = bf16_lo(kp) * cscale;
+        sScale[(s & (kScaleBufs - 1)) * 2 * BK + BK + key] = bf16_lo(vp);
         tc_fence_after();
         zero_pairs(kp, z24, z20);
 #pragma unroll
@@ -464,15 +470,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_ready[bf]);
       }
-      if (doV) {
+      if (doV && s >= kLag) {
+        const int t = s - kLag, st = t % C::kStages, bf = t & 1;
+        ok = mbar_wait_warp(&code_full[st], (uint32_t)(t / C::kStages) & 1u, abort_flag);
+        if (!ok) break;
+        const uint8_t* row = sCode + st * kStage + kCodeTile + key * 64;
+        const uint32_t vp = ((const uint32_t*)(sCode + st * kStage + 2 * kCodeTile))[BK + key];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(&w[4 * i]) =
-              *reinterpret_cast<const uint4*>(row + kCodeTile + ((i ^ sw) << 4));
+          *reinterpret_cast<uint4*>(&w[4 * i]) = *reinterpret_cast<const uint4*>(row + ((i ^ sw) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&code_empty[st]);
         if (t >= 2) {  // PV(t - 2) has read this V buffer
-          if (!mbar_wait_warp(&pv_done[bf], prev, abort_flag)) break;
+          ok = mbar_wait_warp(&pv_done[bf], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
         }
         zero_pairs(vp, z24, z20);
         uint8_t* dst = sV + bf * kVTile + key * 128;
