@@ -57,12 +57,13 @@ constexpr uint32_t kStage = 2 * kCodeTile + 2 * BK * 4;  // K | V codes, K | V (
 constexpr int kScaleBufs = 4;
 
 // Warpgroups: 0 TMA and MMA issue, then unpack, then two of softmax.  Up to
-// 64 query rows the two softmax warpgroups take alternate key tiles, all rows
+// 32 query rows the two softmax warpgroups take alternate key tiles, all rows
 // each, with their own maxima, sums and O^T (merged at the end): a tile's
-// chain of waits may then last two tiles.  128 rows are split in halves.
+// chain of waits may then last two tiles.  64 and 128 rows are split in halves
+// (at 64 rows, 37 heads x 4 sequences of 8K: halves 104 us, alternate tiles 121).
 template <int NC>
 struct Cfg {
-  static constexpr int kSets = NC <= 64 ? 2 : 1;
+  static constexpr int kSets = NC <= 32 ? 2 : 1;
   static constexpr int CP = kSets == 2 ? NC : NC / 2;  // query rows per softmax thread
   static constexpr int BS = CP < 32 ? CP : 32;         // of them in one mask word
   static constexpr int NB = CP / BS;
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
             const __half2 hh = __floats2half2_rn(a, d);
             h[e] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          *reinterpret_cast<uint4*>(prow + ((c8 ^ (key & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(prow + (((((col0 & 63) >> 3) + c8) ^ (key & 7)) << 4)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
       };
