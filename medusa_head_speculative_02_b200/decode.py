@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import api
-from .step import VerifyStep
+from .step import PackedVerifyStep, VerifyStep
 from .synthetic import MedusaConfig
 
 
@@ -27,15 +27,17 @@ class DecodeLoop:
 
     ``max_steps`` sizes the cache headroom: each step appends at most K + 1
     slots per sequence, so L_b + N <= Lcap holds for that many steps.
+    ``packed`` keeps the cache in 4 bits; ``window`` > 0 restricts attention
+    to that many recent positions and the first ``sinks``.
     """
 
     def __init__(self, cfg: MedusaConfig, device="cuda", seed: int = 0, max_steps: int = 64,
-                 sample_temperature=None, sample_seed: int = 0):
+                 sample_temperature=None, sample_seed: int = 0, packed: bool = False,
+                 window: int = 0, sinks: int = 0):
         self.cfg = cfg.scaled(headroom=cfg.headroom + max_steps * (cfg.K + 1))
         self.max_steps = int(max_steps)
-        self.st = VerifyStep(self.cfg, device, seed)
-        x = self.st.x
-        self._init = {k: x[k].clone() for k in ("prefix_len", "root_tok", "k_cache", "v_cache")}
+        self.st = (PackedVerifyStep if packed else VerifyStep)(self.cfg, device, seed, window, sinks)
+        self._init = {k: v.clone() for k, v in self.st.state().items()}
         self.sample_temperature = sample_temperature
         self.sample_seed = int(sample_seed)
         self.draws = torch.zeros(1, dtype=torch.int64, device=self.st.dev)  # noise offset
@@ -45,8 +47,8 @@ class DecodeLoop:
     def reset(self) -> None:
         """Back to the state before the first step (prefix lengths, roots,
         cache, draw counter)."""
-        for k, v in self._init.items():
-            self.st.x[k].copy_(v)
+        for k, v in self.st.state().items():
+            v.copy_(self._init[k])
         self.draws.zero_()
         self.steps_done = 0
 

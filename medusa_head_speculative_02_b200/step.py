@@ -22,8 +22,13 @@ LAUNCHES = {"heads": 4, "build_tree": 1, "accept": 2, "kv_compact": 1}
 
 
 class VerifyStep:
-    def __init__(self, cfg: MedusaConfig, device="cuda", seed: int = 0):
+    """One verify step with a bf16/fp32 KV cache; window > 0: tree attention
+    with a sliding window of that many positions and the first `sinks`."""
+
+    def __init__(self, cfg: MedusaConfig, device="cuda", seed: int = 0, window: int = 0,
+                 sinks: int = 0):
         self.cfg = cfg
+        self.window, self.sinks = int(window), int(sinks)
         self.dev = torch.device(device)
         self.x = gen_inputs(cfg, self.dev, seed)
         self.tree = api.Tree(cfg.K, cfg.s, cfg.N)
@@ -43,9 +48,8 @@ class VerifyStep:
         self.new_len = torch.empty(B, **i32)
         self.ws_heads = torch.empty(api.heads_workspace_size(B, cfg.d, cfg.V, K, s, cfg.torch_dtype),
                                     dtype=torch.uint8, device=self.dev)
-        self.ws_attn = torch.empty(max(256, api.attention_workspace_size(self.tree, B, cfg.Hq,
-                                                                         cfg.Hkv, cfg.dh, cfg.Lcap)),
-                                   dtype=torch.uint8, device=self.dev)
+        self.ws_attn = torch.empty(max(256, self._attention_workspace()), dtype=torch.uint8,
+                                   device=self.dev)
         self.ws_acc = torch.empty(max(256, api.accept_workspace_size(self.tree, B, cfg.V)),
                                   dtype=torch.uint8, device=self.dev)
         self.scale = 1.0 / math.sqrt(cfg.dh)
@@ -55,6 +59,17 @@ class VerifyStep:
         torch.cuda.synchronize(self.dev)
         parent = self.tree.info()[0]
         self.vlogits = plant_verify_logits(cfg, parent, self.tree_tok.cpu(), self.dev, seed)
+
+    def _attention_workspace(self) -> int:
+        c = self.cfg
+        if self.window:
+            return api.attention_window_workspace_size(self.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap,
+                                                       c.torch_dtype, self.window, self.sinks)
+        return api.attention_workspace_size(self.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap)
+
+    def state(self) -> dict:
+        """The tensors a step changes or continues from."""
+        return {k: self.x[k] for k in ("prefix_len", "root_tok", "k_cache", "v_cache")}
 
     # individual calls --------------------------------------------------------
     def heads(self):
@@ -69,6 +84,11 @@ class VerifyStep:
 
     def attention(self):
         x = self.x
+        if self.window:
+            api.medusa_tree_attention_window(x["q"], x["k_cache"], x["v_cache"], x["prefix_len"],
+                                             self.tree, self.scale, self.window, self.sinks,
+                                             out=self.attn_out, ws=self.ws_attn)
+            return
         api.medusa_tree_attention(x["q"], x["k_cache"], x["v_cache"], x["prefix_len"], self.tree,
                                   self.scale, out=self.attn_out, ws=self.ws_attn)
 
@@ -106,7 +126,10 @@ class VerifyStep:
         c = self.cfg
         # both rules: one row reduction and two walks
         acc = LAUNCHES["accept"] + 1 if c.accept == "both" else LAUNCHES["accept"]
-        attn = api.attention_launches(self.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap, c.torch_dtype)
+        if self.window:  # a workspace is asked for exactly when a second kernel merges chunks
+            attn = 1 + (self._attention_workspace() > 0)
+        else:
+            attn = api.attention_launches(self.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap, c.torch_dtype)
         return (LAUNCHES["heads"] + LAUNCHES["build_tree"] + attn + acc + LAUNCHES["kv_compact"])
 
     # algorithmic work ---------------------------------------------------------
@@ -121,6 +144,66 @@ class VerifyStep:
     def attention_bytes(self) -> int:
         """K/V actually read (prefix + tree slots) + Q + O."""
         return kernel_bench.attention_bytes(self.cfg, int(self.x["prefix_len"].sum().item()))
+
+
+class PackedVerifyStep(VerifyStep):
+    """A verify step on a 4-bit KV cache, optionally windowed: heads, tree
+    expansion, the tree tokens' K/V stored at slots L_b .. L_b + N - 1, tree
+    attention over the 4-bit cache, acceptance, compaction.  The prefix is
+    stored once at construction; tree_k, tree_v [B][N][Hkv][dh] are the tree
+    tokens' K/V of every step (there is no base model to produce new ones)."""
+
+    def __init__(self, cfg: MedusaConfig, device="cuda", seed: int = 0, window: int = 0,
+                 sinks: int = 0):
+        self.Lcap = (cfg.Lcap + 3) // 4 * 4  # the 4-bit cache's capacity is a multiple of 4
+        super().__init__(cfg, device, seed, window, sinks)
+        x, c = self.x, cfg
+        self.cache = api.PackedCache.empty(c.B, c.Hkv, self.Lcap, c.dh, self.dev)
+        zero = torch.zeros(c.B, dtype=torch.int32, device=self.dev)
+        api.medusa_kv_pack(x["k_cache"], x["v_cache"], self.cache, zero, x["prefix_len"])
+        slot = x["prefix_len"].long()[:, None] + torch.arange(c.N, device=self.dev)
+        b = torch.arange(c.B, device=self.dev)[:, None]
+        self.tree_k = x["k_cache"][b, slot].contiguous()
+        self.tree_v = x["v_cache"][b, slot].contiguous()
+        del x["k_cache"], x["v_cache"]
+
+    def _attention_workspace(self) -> int:
+        c = self.cfg
+        return api.attention_packed_workspace_size(self.tree, c.B, c.Hq, c.Hkv, c.dh, self.Lcap,
+                                                   c.torch_dtype, self.window, self.sinks)
+
+    def state(self) -> dict:
+        c = self.cache
+        return {"prefix_len": self.x["prefix_len"], "root_tok": self.x["root_tok"],
+                "k_codes": c.k_codes, "k_par": c.k_par, "v_codes": c.v_codes, "v_par": c.v_par}
+
+    def store(self):
+        api.medusa_kv_pack(self.tree_k, self.tree_v, self.cache, self.x["prefix_len"])
+
+    def attention(self):
+        api.medusa_tree_attention_packed(self.x["q"], self.cache, self.x["prefix_len"], self.tree,
+                                         self.scale, self.window, self.sinks, out=self.attn_out,
+                                         ws=self.ws_attn)
+
+    def compact(self):
+        api.medusa_kv_compact_packed(self.cache, self.x["prefix_len"], self.accept_len,
+                                     self.accept_nodes, self.cfg.K, new_len=self.new_len)
+
+    def run(self):
+        self.heads()
+        self.build_tree()
+        self.store()
+        self.attention()
+        self.accept()
+        self.compact()
+
+    def launches_per_step(self) -> int:
+        acc = LAUNCHES["accept"] + 1 if self.cfg.accept == "both" else LAUNCHES["accept"]
+        attn = 1 + (self._attention_workspace() > 0)  # a second kernel merges key chunks
+        return (LAUNCHES["heads"] + LAUNCHES["build_tree"] + 1 + attn + acc + LAUNCHES["kv_compact"])
+
+    def attention_bytes(self) -> int:
+        raise NotImplementedError("counted for the bf16/fp32 cache only")
 
 
 class MultiLayerStep:
