@@ -160,7 +160,7 @@ __device__ __forceinline__ void red_consume(RedState& st, const float (&x)[NV], 
 // Chunk sp of verify row `row` reduced by one CTA: the argmax key and, with
 // TYPICAL, the softmax statistics at scale zscale.
 template <typename T, bool TYPICAL>
-__device__ __forceinline__ void row_reduce_chunk(const T* __restrict__ vlog, int V, int chunk,
+__device__ __forceinline__ void row_reduce_chunk(const T* vlog, int V, int chunk,
                                                  int splits, float zscale, size_t row, int sp,
                                                  RowPart* __restrict__ parts) {
   const int lo = sp * chunk;
@@ -251,7 +251,7 @@ __device__ __forceinline__ void row_reduce_chunk(const T* __restrict__ vlog, int
 // leaf ends the accepted path) and reports (m, Z, S) = (-inf, 0, 0).
 template <typename T, bool TYPICAL>
 __global__ void __launch_bounds__(kRedThreads)
-    row_reduce_kernel(const T* __restrict__ vlog, int V, int chunk, int splits, ZTab zt,
+    row_reduce_kernel(const T* vlog, int V, int chunk, int splits, ZTab zt,
                       const int32_t* __restrict__ depth, const int32_t* __restrict__ nchild,
                       int N, int K, RowPart* __restrict__ parts) {
   // nothing in this kernel runs ahead of its predecessor
@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kRedThreads)
 // a whole warp, <= MEDUSA_MAX_N).
 template <typename T, bool TYPICAL>
 __global__ void __launch_bounds__(MEDUSA_MAX_N)
-    accept_walk_kernel(const T* __restrict__ vlog, const RowPart* __restrict__ parts, int splits,
-                       const int32_t* __restrict__ tok, const int32_t* __restrict__ parent,
+    accept_walk_kernel(const T* vlog, const RowPart* parts, int splits,
+                       const int32_t* tok, const int32_t* __restrict__ parent,
                        const int32_t* __restrict__ depth, const uint32_t* __restrict__ anc, int N,
                        int W, int K, int V, ZTab zt, float eps, float delta,
                        int32_t* __restrict__ accept_len, int32_t* __restrict__ accept_nodes,

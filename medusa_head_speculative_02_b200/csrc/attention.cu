@@ -61,8 +61,8 @@ AttnPlan make_plan(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lca
 // grid: (rblocks, chunks, B*Hkv)
 template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads)
-    tree_attn_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc,
-                          const T* __restrict__ vc, const int32_t* __restrict__ Lp,
+    tree_attn_simt_kernel(const T* q, const T* kc,
+                          const T* vc, const int32_t* Lp,
                           const uint32_t* __restrict__ anc, int N, int W, int Hq, int Hkv,
                           int Lcap, float qscale, int P, int R, float* __restrict__ po,
                           float2* __restrict__ pml) {
@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(kThreads)
 
 // One warp per output row (b, node, h): merge the chunks.
 template <typename T, int DH>
-__global__ void tree_attn_combine_kernel(const float* __restrict__ po,
-                                         const float2* __restrict__ pml,
-                                         const int32_t* __restrict__ Lp, int B, int N, int Hq,
+__global__ void tree_attn_combine_kernel(const float* po,
+                                         const float2* pml,
+                                         const int32_t* Lp, int B, int N, int Hq,
                                          int Hkv, int Lcap, int chunks, int R,
                                          T* __restrict__ out) {
   // nothing in this kernel runs ahead of its predecessor

@@ -234,9 +234,8 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     qv[i] = make_uint2(0u, 0u);
     if (r < p.R) {
       const int node = r / p.G, g = r - node * p.G;
-      qv[i] = __ldg(reinterpret_cast<const uint2*>(
-                        p.q + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH) +
-                    lane);
+      qv[i] = reinterpret_cast<const uint2*>(
+          p.q + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH)[lane];
     }
     const float f[4] = {bf16_lo(qv[i].x), bf16_hi(qv[i].x), bf16_lo(qv[i].y), bf16_hi(qv[i].y)};
 #pragma unroll

@@ -623,7 +623,9 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Programmatic dependent launch: wait until every kernel this one depends on
-// has completed and its memory is visible; let the next kernel in the stream
+// has completed and its memory is visible (a kernel must not take data that
+// another one writes as `const T* __restrict__` or through __ldg: such loads
+// count as constant for the whole kernel and were moved ahead of this wait); let the next kernel in the stream
 // be scheduled (it still waits in its own griddepcontrol.wait).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {

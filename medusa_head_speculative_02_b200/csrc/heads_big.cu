@@ -520,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // u[k][b] = SiLU(sum of the K-split partials + b1[k]) + h[b], written as the
 // bf16 pair (hi, lo = u - hi) in rows 2b, 2b + 1 of stage 2's B operand.
 // One thread per (head, sequence, feature), coalesced over the feature.
-__global__ void heads_big_silu_kernel(const float* __restrict__ part, int S, int K, int B, int d,
+__global__ void heads_big_silu_kernel(const float* part, int S, int K, int B, int d,
                                       const __nv_bfloat16* __restrict__ b1,
-                                      const __nv_bfloat16* __restrict__ h,
+                                      const __nv_bfloat16* h,
                                       __nv_bfloat16* __restrict__ u) {
   griddep_launch_dependents();  // stage 2 may take its TMEM and wait
   griddep_wait();

@@ -24,9 +24,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // stage 1 writes u[kh][b][m] = SiLU(acc + b1) + h; stage 2 writes
 // logits[b][kh][m] = acc.
 __global__ void __launch_bounds__(kWarps * 32)
-    heads_simt_kernel(int stage, const float* __restrict__ W, const float* __restrict__ x,
+    heads_simt_kernel(int stage, const float* __restrict__ W, const float* x,
                       size_t x_stride_k, const float* __restrict__ b1,
-                      const float* __restrict__ h, float* __restrict__ out, int B, int d,
+                      const float* h, float* __restrict__ out, int B, int d,
                       int rows_per_head, int K) {
   // nothing in this kernel runs ahead of its predecessor
   griddep_launch_dependents();
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int b = 0; b < kBmax; ++b) {
       if (b < B) {
-        const float4 xv = __ldg(reinterpret_cast<const float4*>(xk + (size_t)b * d) + i);
+        const float4 xv = reinterpret_cast<const float4*>(xk + (size_t)b * d)[i];
         acc[b] += w.x * xv.x + w.y * xv.y + w.z * xv.z + w.w * xv.w;
       }
     }

@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // u[k][b] = SiLU(sum of the K-split partials + b1[k]) + h[b], stored as the
 // bf16 pair (hi, lo = u - hi) in rows 2b, 2b+1 of stage 2's B operand.
 // It also zeroes the split counters of stage 2, which runs next.
-__global__ void heads_silu_kernel(const float* __restrict__ part, int S, int K, int B, int d,
+__global__ void heads_silu_kernel(const float* part, int S, int K, int B, int d,
                                   const __nv_bfloat16* __restrict__ b1,
-                                  const __nv_bfloat16* __restrict__ h,
+                                  const __nv_bfloat16* h,
                                   __nv_bfloat16* __restrict__ u, int* __restrict__ cnt2,
                                   int ncnt2) {
   griddep_launch_dependents();  // stage 2 may start streaming its weights

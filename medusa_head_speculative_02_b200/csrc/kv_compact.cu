@@ -19,9 +19,9 @@ namespace {
 
 template <typename VecT>
 __global__ void kv_compact_kernel(VecT* __restrict__ kc, VecT* __restrict__ vc,
-                                  const int32_t* __restrict__ L,
-                                  const int32_t* __restrict__ alen,
-                                  const int32_t* __restrict__ anodes, int Lcap, int K,
+                                  const int32_t* L,
+                                  const int32_t* alen,
+                                  const int32_t* anodes, int Lcap, int K,
                                   size_t slot_vecs, size_t layer_vecs,
                                   int32_t* __restrict__ new_len) {
   // nothing in this kernel runs ahead of its predecessor

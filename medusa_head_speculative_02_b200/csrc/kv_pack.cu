@@ -120,8 +120,8 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
 // (b, t, h) of row `row` of [B][T][H], and the cache row it goes to (or -1:
 // not one of the sequence's tokens, or outside the cache).
 __device__ __forceinline__ long long cache_row(long long row, int T, int H, int Lcap,
-                                               const int32_t* __restrict__ start,
-                                               const int32_t* __restrict__ count) {
+                                               const int32_t* start,
+                                               const int32_t* count) {
   const long long bt = row / H;
   const int h = (int)(row - bt * H);
   const long long b = bt / T;
@@ -136,8 +136,8 @@ __device__ __forceinline__ long long cache_row(long long row, int T, int H, int 
 // flight at once.
 template <typename T, int DH, int RPT>
 __global__ void __launch_bounds__(kThreads)
-    kv_pack_kernel(const T* __restrict__ k, const T* __restrict__ v,
-                   const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+    kv_pack_kernel(const T* k, const T* v,
+                   const int32_t* start, const int32_t* count,
                    long long rows, int Tn, int H, int Lcap, uint32_t* __restrict__ kc,
                    uint32_t* __restrict__ kp, uint32_t* __restrict__ vc,
                    uint32_t* __restrict__ vp) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads)
   griddep_wait();
   constexpr int LPR = DH / 8;
   constexpr int GROUPS = kThreads / LPR;
-  const T* __restrict__ src = blockIdx.y ? v : k;
+  const T* src = blockIdx.y ? v : k;
   uint32_t* __restrict__ codes = blockIdx.y ? vc : kc;
   uint32_t* __restrict__ par = blockIdx.y ? vp : kp;
   const int sub = threadIdx.x % LPR;
@@ -175,17 +175,17 @@ __global__ void __launch_bounds__(kThreads)
 // count and outside the cache.
 template <typename T, int DH, int RPT>
 __global__ void __launch_bounds__(kThreads)
-    kv_unpack_kernel(const uint32_t* __restrict__ kc, const uint32_t* __restrict__ kp,
-                     const uint32_t* __restrict__ vc, const uint32_t* __restrict__ vp,
-                     const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+    kv_unpack_kernel(const uint32_t* kc, const uint32_t* kp,
+                     const uint32_t* vc, const uint32_t* vp,
+                     const int32_t* start, const int32_t* count,
                      long long rows, int Tn, int H, int Lcap, T* __restrict__ k,
                      T* __restrict__ v) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int LPR = DH / 8;
   constexpr int GROUPS = kThreads / LPR;
-  const uint32_t* __restrict__ codes = blockIdx.y ? vc : kc;
-  const uint32_t* __restrict__ par = blockIdx.y ? vp : kp;
+  const uint32_t* codes = blockIdx.y ? vc : kc;
+  const uint32_t* par = blockIdx.y ? vp : kp;
   T* __restrict__ out = blockIdx.y ? v : k;
   const int sub = threadIdx.x % LPR;
   const long long row0 = (long long)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     kv_compact_packed_kernel(uint32_t* __restrict__ kc, uint32_t* __restrict__ kp,
                              uint32_t* __restrict__ vc, uint32_t* __restrict__ vp,
-                             const int32_t* __restrict__ L, const int32_t* __restrict__ alen,
-                             const int32_t* __restrict__ anodes, long long total, int B, int H,
+                             const int32_t* L, const int32_t* alen,
+                             const int32_t* anodes, long long total, int B, int H,
                              int words, int Lcap, int K, int32_t* __restrict__ new_len) {
   griddep_launch_dependents();
   griddep_wait();

@@ -41,10 +41,10 @@ __device__ __forceinline__ uint64_t splitmix64_at(uint64_t seed, uint64_t idx) {
 // reads the others' best keys from their shared memory (DSMEM).
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    sample_next_kernel(const T* __restrict__ vlog, const int32_t* __restrict__ alen,
-                       const int32_t* __restrict__ anodes, int B, int N, int V, int K,
+    sample_next_kernel(const T* vlog, const int32_t* alen,
+                       const int32_t* anodes, int B, int N, int V, int K,
                        int greedy, float inv_t, uint64_t seed, uint64_t offset,
-                       const uint64_t* __restrict__ offset_dev, int32_t* __restrict__ next_tok) {
+                       const uint64_t* offset_dev, int32_t* __restrict__ next_tok) {
   // nothing in this kernel runs ahead of its predecessor
   griddep_launch_dependents();
   griddep_wait();

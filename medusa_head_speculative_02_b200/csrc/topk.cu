@@ -36,7 +36,7 @@ __device__ __forceinline__ void block_select(uint64_t (&k)[kSmax], int s, uint64
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) topk_rows_kernel(const T* __restrict__ x, int V, int s,
+__global__ void __launch_bounds__(kThreads) topk_rows_kernel(const T* x, int V, int s,
                                                              int32_t* __restrict__ idx,
                                                              float* __restrict__ val) {
   // nothing in this kernel runs ahead of its predecessor
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) topk_rows_kernel(const T* __restrict
   if ((V % VEC) == 0 && (((uintptr_t)xr) & 15u) == 0) {
     const int nv = V / VEC;
     for (int i = threadIdx.x; i < nv; i += kThreads) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(xr) + i);
+      const uint4 w = reinterpret_cast<const uint4*>(xr)[i];
       const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) topk_rows_kernel(const T* __restrict
 }
 
 // Rows of pre-built candidate keys (0 = empty).
-__global__ void __launch_bounds__(kThreads) topk_keys_kernel(const uint64_t* __restrict__ keys,
+__global__ void __launch_bounds__(kThreads) topk_keys_kernel(const uint64_t* keys,
                                                              int C, int s,
                                                              int32_t* __restrict__ idx,
                                                              float* __restrict__ val) {
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kThreads) topk_keys_kernel(const uint64_t* __r
 // descending, ties to the lower index; shard g's indices are offset by v0[g]
 // (device array) when v0 is given.
 __global__ void __launch_bounds__(kThreads)
-    topk_merge_kernel(const float* __restrict__ val, const int32_t* __restrict__ idx,
-                      long long gs, const int32_t* __restrict__ v0, int G, int R, int c, int s,
+    topk_merge_kernel(const float* val, const int32_t* idx,
+                      long long gs, const int32_t* v0, int G, int R, int c, int s,
                       int32_t* __restrict__ out_idx, float* __restrict__ out_val) {
   // nothing in this kernel runs ahead of its predecessor
   griddep_launch_dependents();

@@ -11,9 +11,9 @@ namespace {
 
 __global__ void build_tree_kernel(const int32_t* __restrict__ head_rank,
                                   const int32_t* __restrict__ depth,
-                                  const int32_t* __restrict__ root,
-                                  const int32_t* __restrict__ topk,
-                                  const int32_t* __restrict__ L, int B, int N, int Ks,
+                                  const int32_t* root,
+                                  const int32_t* topk,
+                                  const int32_t* L, int B, int N, int Ks,
                                   int32_t* __restrict__ tok, int32_t* __restrict__ pos) {
   // nothing in this kernel runs ahead of its predecessor
   griddep_launch_dependents();
