@@ -56,29 +56,37 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
 
-// rint(x / s) as the correctly rounded fp32 quotient gives it, r = 1 / s.
-// x * r is within 2e-6 of the quotient (|x / s| <= 16), so its rounding
-// decides unless it lies that close to a tie; only then is the division done.
-__device__ __forceinline__ float rint_div(float x, float s, float r) {
-  const float q = x * r;
-  const float n = rintf(q);
-  if (fabsf(fabsf(q - n) - 0.5f) > 1e-5f) return n;
-  return rintf(__fdiv_rn(x, s));
+// The codes of 8 values, divided: rint of the correctly rounded quotients.
+__device__ __forceinline__ uint32_t codes_by_division(const float (&x)[8], float s, float zero) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + zero, 0.f), 15.f);
+    w |= (uint32_t)(int)c << (4 * i);
+  }
+  return w;
 }
 
 // Encodes one row held 8 values to a lane by LPR neighbouring lanes: this
 // lane's code word, and the row's (scale, zero) word.
+//
+// rint(x / s): x times the hardware's 1 / s (1 ulp) is within 4e-6 of the
+// quotient (|x / s| < 16), so its nearest integer is the quotient's unless it
+// lies that close to a tie; only a lane with such a value divides (a lane in
+// 3000).  Adding 1.5 * 2^23 rounds to nearest even and leaves the integer in
+// the low bits, so no conversion instruction is used (rint and float-to-int run
+// at an eighth of the rate of an addition).  A code is never negative: rint is
+// odd and monotone, so rint(x / s) >= rint(lo / s) = -zero.
 template <int LPR>
 __device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
-  float lo = 0.f, hi = 0.f;
-  bool bad = false;
+  float lo = 0.f, hi = 0.f, nan = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
-    bad |= !(fabsf(x[i]) <= 3.4028234e38f);  // NaN or infinity
+    nan = fmaf(x[i], 0.f, nan);  // NaN from a NaN or an infinity
   }
-  if (bad) hi = INFINITY;  // reaches every lane through the row maximum
+  if (nan != 0.f) hi = INFINITY;  // reaches every lane through the row maximum
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -94,79 +102,99 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
     par = 0u;
     return 0u;
   }
-  float zero;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  const float qz = -lo * r, tz = __fadd_rn(qz, kMagic);
+  float far = fabsf(qz - __fsub_rn(tz, kMagic));  // largest distance from an integer
+  const int zi = __float_as_int(tz) - 0x4b400000;
+  const int bias = zi - 0x4b400000;
   uint32_t w = 0u;
-  if (s < 1e-30f) {  // 1 / s may overflow: divide
-    zero = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + zero, 0.f), 15.f);
-      w |= (uint32_t)(int)c << (4 * i);
-    }
-  } else {
-    const float r = __frcp_rn(s);
-    zero = fminf(fmaxf(rint_div(-lo, s, r), 0.f), 15.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rint_div(x[i], s, r) + zero, 0.f), 15.f);
-      w |= (uint32_t)(int)c << (4 * i);
-    }
+  for (int i = 7; i >= 0; --i) {
+    const float q = x[i] * r;
+    const float t = __fadd_rn(q, kMagic);
+    far = fmaxf(far, fabsf(q - __fsub_rn(t, kMagic)));
+    w = w * 16u + (uint32_t)__viaddmin_s32(__float_as_int(t), bias, 15);
   }
-  par = (uint32_t)__bfloat16_as_ushort(sb) |
-        ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(zero)) << 16);
+  float zero = __fsub_rn(tz, kMagic);
+  // (far is the lane's own: every lane of a row finds the same zero either way)
+  if (!(far <= 0.49999f) || s < 1e-30f) {  // (1 / s may overflow for the smallest scales)
+    zero = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
+    w = codes_by_division(x, s, zero);
+  }
+  par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(zero) & 0xffff0000u);
   return w;
 }
 
-// (b, t, h) of row `row` of [B][T][H], and the cache row it goes to (or -1:
-// not one of the sequence's tokens, or outside the cache).
-__device__ __forceinline__ long long cache_row(long long row, int T, int H, int Lcap,
-                                               const int32_t* start,
-                                               const int32_t* count) {
-  const long long bt = row / H;
-  const int h = (int)(row - bt * H);
-  const long long b = bt / T;
-  const int t = (int)(bt - b * T);
-  if (count != nullptr && t >= count[b]) return -1;
-  const long long slot = (long long)start[b] + t;
-  if (slot < 0 || slot >= Lcap) return -1;
-  return (b * H + h) * Lcap + slot;
+// idx / d for idx < 2^31 with m = floor(2^32 / d) (d = 1: 2^32 - 1): the high
+// product is at most 2 short.
+__device__ __forceinline__ uint32_t fast_div(uint32_t idx, uint32_t d, uint32_t m) {
+  uint32_t q = __umulhi(idx, m);
+  uint32_t r = idx - q * d;
+  if (r >= d) {
+    ++q;
+    r -= d;
+  }
+  return r >= d ? q + 1 : q;
 }
 
-// Rows [B][T][H] of K (grid y 0) and V (grid y 1); RPT rows per lane group in
-// flight at once.
+// Grid: x over the (token, head) rows of a sequence, y the sequences, z K and
+// V; RPT rows per lane group in flight at once.  The rows' slots are those of
+// tokens start_b + t, t < count_b.
+struct RowGrid {
+  const int32_t* start;
+  const int32_t* count;
+  int B, T, H, Lcap;
+  uint32_t rows, hmul;  // T * H, floor(2^32 / H)
+};
+
+// Cache row of row `row` of sequence b, or -1: not one of its tokens, or
+// outside the cache.
+__device__ __forceinline__ long long cache_row(const RowGrid& g, int b, int start, int count,
+                                               uint32_t row) {
+  if (row >= g.rows) return -1;
+  const uint32_t t = fast_div(row, g.H, g.hmul);
+  const int h = (int)(row - t * g.H);
+  const long long slot = (long long)start + t;
+  if ((long long)t >= count || slot < 0 || slot >= g.Lcap) return -1;
+  return ((long long)b * g.H + h) * g.Lcap + slot;
+}
+
 template <typename T, int DH, int RPT>
 __global__ void __launch_bounds__(kThreads)
-    kv_pack_kernel(const T* k, const T* v,
-                   const int32_t* start, const int32_t* count,
-                   long long rows, int Tn, int H, int Lcap, uint32_t* __restrict__ kc,
-                   uint32_t* __restrict__ kp, uint32_t* __restrict__ vc,
-                   uint32_t* __restrict__ vp) {
+    kv_pack_kernel(const T* k, const T* v, const RowGrid g, uint32_t* kc, uint32_t* kp,
+                   uint32_t* vc, uint32_t* vp) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int LPR = DH / 8;
   constexpr int GROUPS = kThreads / LPR;
-  const T* src = blockIdx.y ? v : k;
-  uint32_t* __restrict__ codes = blockIdx.y ? vc : kc;
-  uint32_t* __restrict__ par = blockIdx.y ? vp : kp;
+  const T* src = blockIdx.z ? v : k;
+  uint32_t* codes = blockIdx.z ? vc : kc;
+  uint32_t* par = blockIdx.z ? vp : kp;
   const int sub = threadIdx.x % LPR;
-  const long long row0 = (long long)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
-  float x[RPT][8];
-  long long dst[RPT];
+  const uint32_t first = blockIdx.x * (GROUPS * RPT);
+  for (int b = blockIdx.y; b < g.B; b += gridDim.y) {
+    const int count = g.count ? g.count[b] : g.T, start = g.start[b];
+    if (count <= 0 || (long long)first >= (long long)count * g.H) continue;  // (uniform) past its tokens
+    float x[RPT][8];
+    long long dst[RPT];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const long long row = row0 + (long long)i * GROUPS;
-    dst[i] = row < rows ? cache_row(row, Tn, H, Lcap, start, count) : -1;
+    for (int i = 0; i < RPT; ++i) {
+      const uint32_t row = first + threadIdx.x / LPR + i * GROUPS;
+      dst[i] = cache_row(g, b, start, count, row);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-    if (dst[i] >= 0) load8(src + row * DH + sub * 8, x[i]);
-  }
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      if (dst[i] >= 0) load8(src + ((size_t)b * g.rows + row) * DH + sub * 8, x[i]);
+    }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    uint32_t p;
-    const uint32_t w = encode<LPR>(x[i], p);  // every lane: the row maxima are shuffles
-    if (dst[i] >= 0) {
-      codes[dst[i] * LPR + sub] = w;
-      if (sub == 0) par[dst[i]] = p;
+    for (int i = 0; i < RPT; ++i) {
+      uint32_t p;
+      const uint32_t w = encode<LPR>(x[i], p);  // every lane: the row maxima are shuffles
+      if (dst[i] >= 0) {
+        codes[dst[i] * LPR + sub] = w;
+        if (sub == 0) par[dst[i]] = p;
+      }
     }
   }
 }
@@ -175,37 +203,38 @@ __global__ void __launch_bounds__(kThreads)
 // count and outside the cache.
 template <typename T, int DH, int RPT>
 __global__ void __launch_bounds__(kThreads)
-    kv_unpack_kernel(const uint32_t* kc, const uint32_t* kp,
-                     const uint32_t* vc, const uint32_t* vp,
-                     const int32_t* start, const int32_t* count,
-                     long long rows, int Tn, int H, int Lcap, T* __restrict__ k,
-                     T* __restrict__ v) {
+    kv_unpack_kernel(const uint32_t* kc, const uint32_t* kp, const uint32_t* vc,
+                     const uint32_t* vp, const RowGrid g, T* k, T* v) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int LPR = DH / 8;
   constexpr int GROUPS = kThreads / LPR;
-  const uint32_t* codes = blockIdx.y ? vc : kc;
-  const uint32_t* par = blockIdx.y ? vp : kp;
-  T* __restrict__ out = blockIdx.y ? v : k;
+  const uint32_t* codes = blockIdx.z ? vc : kc;
+  const uint32_t* par = blockIdx.z ? vp : kp;
+  T* out = blockIdx.z ? v : k;
   const int sub = threadIdx.x % LPR;
-  const long long row0 = (long long)blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
-  uint32_t w[RPT], p[RPT];
+  for (int b = blockIdx.y; b < g.B; b += gridDim.y) {
+    const int count = g.count ? g.count[b] : g.T, start = g.start[b];
+    const uint32_t row0 = blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
+    uint32_t w[RPT], p[RPT];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const long long row = row0 + (long long)i * GROUPS;
-    const long long src = row < rows ? cache_row(row, Tn, H, Lcap, start, count) : -1;
-    w[i] = src >= 0 ? codes[src * LPR + sub] : 0u;
-    p[i] = src >= 0 ? par[src] : 0u;
-  }
+    for (int i = 0; i < RPT; ++i) {
+      const long long src = cache_row(g, b, start, count, row0 + i * GROUPS);
+      w[i] = src >= 0 ? codes[src * LPR + sub] : 0u;
+      p[i] = src >= 0 ? par[src] : 0u;
+    }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const long long row = row0 + (long long)i * GROUPS;
-    if (row >= rows) continue;
-    const float s = __uint_as_float(p[i] << 16), z = __uint_as_float(p[i] & 0xffff0000u);
-    float x[8];
+    for (int i = 0; i < RPT; ++i) {
+      const uint32_t row = row0 + i * GROUPS;
+      if (row >= g.rows) continue;
+      const float s = __uint_as_float(p[i] << 16), z = __uint_as_float(p[i] & 0xffff0000u);
+      float x[8];
+      // 2^23 + code by its bits: code - zero is exact either way
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s * ((float)((w[i] >> (4 * e)) & 15u) - z);
-    store8(out + row * DH + sub * 8, x);
+      for (int e = 0; e < 8; ++e)
+        x[e] = s * (__uint_as_float(0x4b000000u | ((w[i] >> (4 * e)) & 15u)) - 8388608.f - z);
+      store8(out + ((size_t)b * g.rows + row) * DH + sub * 8, x);
+    }
   }
 }
 
@@ -262,42 +291,50 @@ __global__ void __launch_bounds__(kThreads)
     if (ok[j - 1]) base[((long long)Lb + j) * stride] = val[j - 1];
 }
 
-int grid_of(long long rows, int per_block, unsigned* g) {
-  const long long n = (rows + per_block - 1) / per_block;
-  if (n > 0x7fffffffLL) return fail(MEDUSA_ERR_UNSUPPORTED, "too many rows for one launch");
-  *g = (unsigned)n;
+// Few rows: one per lane group (latency); many: four in flight.
+int row_grid(const PackedRows& a, int groups, bool* many, RowGrid* g, dim3* grid) {
+  const long long rows = (long long)a.T * a.c.Hkv;
+  if (rows > 0x7fffffffLL - 4 * kThreads)
+    return fail(MEDUSA_ERR_UNSUPPORTED, "T * Hkv does not fit 31 bits");
+  *many = rows * a.B >= 4LL * groups * num_sms();
+  g->start = a.start;
+  g->count = a.count;
+  g->B = a.B;
+  g->T = a.T;
+  g->H = a.c.Hkv;
+  g->Lcap = a.c.Lcap;
+  g->rows = (uint32_t)rows;
+  g->hmul = a.c.Hkv == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)a.c.Hkv);
+  const int per = groups * (*many ? 4 : 1);
+  *grid = dim3((unsigned)((rows + per - 1) / per), (unsigned)(a.B < 65535 ? a.B : 65535), 2);
   return MEDUSA_OK;
 }
 
-// Few rows: one per lane group (latency); many: four in flight.
 template <typename T, int DH>
 int pack_launch_t(const PackedRows& a, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.T * a.c.Hkv;
-  constexpr int GROUPS = kThreads / (DH / 8);
-  const bool many = rows >= 4LL * GROUPS * num_sms();
-  unsigned g;
-  int rc = grid_of(rows, GROUPS * (many ? 4 : 1), &g);
+  bool many = false;
+  RowGrid g = {};
+  dim3 grid;
+  int rc = row_grid(a, kThreads / (DH / 8), &many, &g, &grid);
   if (rc) return rc;
   auto* fn = many ? kv_pack_kernel<T, DH, 4> : kv_pack_kernel<T, DH, 1>;
-  cudaError_t e = launch_pdl(fn, dim3(g, 2), dim3(kThreads), 0, st, (const T*)a.k, (const T*)a.v,
-                             a.start, a.count, rows, a.T, a.c.Hkv, a.c.Lcap, (uint32_t*)a.c.k_codes,
-                             (uint32_t*)a.c.k_par, (uint32_t*)a.c.v_codes, (uint32_t*)a.c.v_par);
+  cudaError_t e = launch_pdl(fn, grid, dim3(kThreads), 0, st, (const T*)a.k, (const T*)a.v, g,
+                             (uint32_t*)a.c.k_codes, (uint32_t*)a.c.k_par, (uint32_t*)a.c.v_codes,
+                             (uint32_t*)a.c.v_par);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "kv_pack_kernel launch");
 }
 template <typename T, int DH>
 int unpack_launch_t(const PackedRows& a, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.T * a.c.Hkv;
-  constexpr int GROUPS = kThreads / (DH / 8);
-  const bool many = rows >= 4LL * GROUPS * num_sms();
-  unsigned g;
-  int rc = grid_of(rows, GROUPS * (many ? 4 : 1), &g);
+  bool many = false;
+  RowGrid g = {};
+  dim3 grid;
+  int rc = row_grid(a, kThreads / (DH / 8), &many, &g, &grid);
   if (rc) return rc;
   auto* fn = many ? kv_unpack_kernel<T, DH, 4> : kv_unpack_kernel<T, DH, 1>;
-  cudaError_t e = launch_pdl(fn, dim3(g, 2), dim3(kThreads), 0, st, (const uint32_t*)a.c.k_codes,
+  cudaError_t e = launch_pdl(fn, grid, dim3(kThreads), 0, st, (const uint32_t*)a.c.k_codes,
                              (const uint32_t*)a.c.k_par, (const uint32_t*)a.c.v_codes,
-                             (const uint32_t*)a.c.v_par, a.start, a.count, rows, a.T, a.c.Hkv,
-                             a.c.Lcap, (T*)a.k_out, (T*)a.v_out);
+                             (const uint32_t*)a.c.v_par, g, (T*)a.k_out, (T*)a.v_out);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "kv_unpack_kernel launch");
 }
@@ -323,10 +360,9 @@ int kv_compact_packed_launch(const PackedCache& c, int layers, int B, const int3
                              cudaStream_t st) {
   const int words = c.dh / 8;
   const long long total = (long long)layers * B * c.Hkv * (2 * words + 2);
-  unsigned g;
-  int rc = grid_of(total > B ? total : B, kThreads, &g);
-  if (rc) return rc;
-  cudaError_t e = launch_pdl(kv_compact_packed_kernel, dim3(g), dim3(kThreads), 0, st,
+  const long long blocks = ((total > B ? total : B) + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffLL) return fail(MEDUSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  cudaError_t e = launch_pdl(kv_compact_packed_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st,
                              (uint32_t*)c.k_codes, (uint32_t*)c.k_par, (uint32_t*)c.v_codes,
                              (uint32_t*)c.v_par, L, alen, anodes, total, B, c.Hkv, words, c.Lcap,
                              K, new_len);
