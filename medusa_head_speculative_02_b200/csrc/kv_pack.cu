@@ -162,7 +162,7 @@ __device__ __forceinline__ long long cache_row(const RowGrid& g, int b, int star
 }
 
 template <typename T, int DH, int RPT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     kv_pack_kernel(const T* k, const T* v, const RowGrid g, uint32_t* kc, uint32_t* kp,
                    uint32_t* vc, uint32_t* vp) {
   griddep_launch_dependents();
@@ -291,7 +291,11 @@ __global__ void __launch_bounds__(kThreads)
     if (ok[j - 1]) base[((long long)Lb + j) * stride] = val[j - 1];
 }
 
-// Few rows: one per lane group (latency); many: four in flight.
+// Few rows: one per lane group (latency); many: four in flight, in 64 registers
+// (16 ragged prompts of up to 8192 tokens, 8 heads: the store takes 181 us, 275
+// with the 90 registers the compiler takes unasked, 198 with two rows in
+// flight, 241 with one).  It is bound by instruction issue (about 200 per 8
+// values: the row's range and the 8 codes), the read back by HBM writes.
 int row_grid(const PackedRows& a, int groups, bool* many, RowGrid* g, dim3* grid) {
   const long long rows = (long long)a.T * a.c.Hkv;
   if (rows > 0x7fffffffLL - 4 * kThreads)
