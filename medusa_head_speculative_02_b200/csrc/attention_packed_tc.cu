@@ -11,7 +11,7 @@
 // Keys are the M dimension.  With 64-node trees and no head grouping a
 // kv-head has 64 query rows, with single tokens a handful, and an MMA is 128
 // rows high; taking the 128 keys of a tile as its rows and the query rows as
-// its N (16 to 128) columns wastes none of it:
+// its N (32, 64 or 128) columns wastes none of it:
 //   S^T [128 keys x NC rows]  = K   (A, from TMEM)  x Q   (B, shared memory)
 //   O^T [128 dims x NC rows] += V^T (A, shared memory, MN-major)
 //                             x P^T (B, shared memory, MN-major)
@@ -30,6 +30,12 @@
 // each thread's registers, one per row, until the end.  Weights times value
 // scales, relative to a power of two >= the largest value scale seen times
 // 2^-7, are rounded once to fp16.  Statistics, sums and products are fp32.
+//
+// What bounds it (64-node trees): the chain products -> softmax -> products of
+// a tile, and per tile and softmax thread the 16 to 64 rows' multiply-add,
+// exponential and rounding.  64 rows, 37 heads x 4 sequences of 8K: 104 us;
+// 64 rows, 32 heads, 2K prefix (the 7B verify step): 23.6 us with the merge,
+// launch to launch, against a cache of 1.6 us of HBM time.
 //
 // TMEM: O^T, two S^T buffers, two K buffers.
 // This source is compiled without relocatable device code: register splits
@@ -65,7 +71,7 @@ template <int NC>
 struct Cfg {
   static constexpr int kSets = NC <= 32 ? 2 : 1;
   static constexpr int CP = kSets == 2 ? NC : NC / 2;  // query rows per softmax thread
-  static constexpr int BS = CP < 32 ? CP : 32;         // of them in one mask word
+  static constexpr int BS = 32;                        // of them in one mask word
   static constexpr int NB = CP / BS;
   static constexpr int kState = 2 * CP;                // (softmax warpgroup, row) states
   static constexpr int kUnpackWgs = NC <= 32 ? 2 : 1;  // K and V apart, or one for both
@@ -131,12 +137,12 @@ __device__ __forceinline__ void zero_pairs(uint32_t par, __half2& z24, __half2& 
   z20 = __float2half2_rn(-z * 0x1p-20f);
 }
 
-// Reduction over the lanes of a warp of N per-lane values each (N = 8, 16, 32),
-// transposed on the way: lane i returns value i mod N over all lanes.
-template <int N, typename Op>
-__device__ __forceinline__ float col_reduce(float (&a)[N], int lane, Op op) {
+// Reduction over the lanes of a warp of 32 per-lane values each, transposed
+// on the way: lane i returns value i over all lanes.
+template <typename Op>
+__device__ __forceinline__ float col_reduce(float (&a)[32], int lane, Op op) {
 #pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) {
+  for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = lane & o;
@@ -144,17 +150,7 @@ __device__ __forceinline__ float col_reduce(float (&a)[N], int lane, Op op) {
       a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  float r = a[0];
-#pragma unroll
-  for (int o = N; o < 32; o <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
-  return r;
-}
-
-template <int SB>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t t, float (&v)[SB]) {
-  if constexpr (SB == 8) tmem_ld8(t, v);
-  else if constexpr (SB == 16) tmem_ld16(t, v);
-  else tmem_ld32(t, v);
+  return a[0];
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -511,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
 #pragma unroll
     for (int c = 0; c < C::CP; ++c) lacc[c] = 0.f;
     float vref = 0x1p-120f;
-    constexpr uint32_t kAll = 0xffffffffu >> (32 - C::BS);
+    constexpr uint32_t kAll = 0xffffffffu;
     uint32_t unset[C::NB];  // rows that have seen no key: their maximum is still open
 #pragma unroll
     for (int n = 0; n < C::NB; ++n) unset[n] = kAll;
@@ -531,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
       // scores relative to the row maxima, base 2
       float y[C::CP];
       if constexpr (C::CP == 64) tmem_ld64(tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0), y);
-      else tmem_ld_cols<C::CP>(tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0), y);
+      else tmem_ld32(tmem + lane_base + C::tS + (uint32_t)(bf * NC + col0), y);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[bf]);
@@ -547,14 +543,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         for (int n = 0; n < C::NB; ++n) {
           if (a0 > -32) {
             // lane c: row c's ancestor bits of this warp's 32 keys, then transposed
-            uint32_t w = 0u;
-            if (lane < C::BS) {
-              const uint32_t* ar = p.anc + (size_t)cnode[col0 + n * C::BS + lane] * p.W;
-              const int wi = a0 >> 5;  // -1: prefix slots first
-              const uint32_t w0 = wi >= 0 && wi < p.W ? __ldg(ar + wi) : 0u;
-              const uint32_t w1 = wi + 1 < p.W ? __ldg(ar + wi + 1) : 0u;
-              w = __funnelshift_r(w0, w1, a0 & 31);
-            }
+            const uint32_t* ar = p.anc + (size_t)cnode[col0 + n * C::BS + lane] * p.W;
+            const int wi = a0 >> 5;  // -1: prefix slots first
+            const uint32_t w0 = wi >= 0 && wi < p.W ? __ldg(ar + wi) : 0u;
+            const uint32_t w1 = wi + 1 < p.W ? __ldg(ar + wi + 1) : 0u;
+            const uint32_t w = __funnelshift_r(w0, w1, a0 & 31);
             uint32_t tm = 0u;
 #pragma unroll
             for (int c = 0; c < C::BS; ++c)
@@ -600,8 +593,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
           float a[C::BS];
 #pragma unroll
           for (int c = 0; c < C::BS; ++c) a[c] = y[n * C::BS + c];
-          const float m = col_reduce<C::BS>(a, lane, [](float x, float z) { return fmaxf(x, z); });
-          if (lane < C::BS) red[(g * 4 + qd) * C::CP + n * C::BS + lane] = m;
+          const float m = col_reduce(a, lane, [](float x, float z) { return fmaxf(x, z); });
+          red[(g * 4 + qd) * C::CP + n * C::BS + lane] = m;
         }
         const uint32_t av = __float_as_uint(fabsf(sv));
         const unsigned sb = __reduce_max_sync(0xffffffffu, av < 0x7f800000u ? av : 0u);
@@ -620,23 +613,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         if (qd == 0) {  // the warpgroup's first warp: lane c is row c of each block
 #pragma unroll
           for (int n = 0; n < C::NB; ++n) {
-            const bool mine = lane < C::BS;
-            const int c = n * C::BS + (mine ? lane : 0);
+            const int c = n * C::BS + lane;
             const float* rr = red + g * 4 * C::CP + c;
             const float x = fmaxf(fmaxf(rr[0], rr[C::CP]), fmaxf(rr[2 * C::CP], rr[3 * C::CP]));
             const bool open = (unset[n] >> lane) & 1u;
-            const bool seen = mine && x != -INFINITY;
+            const bool seen = x != -INFINITY;
             float d = 0.f, f = 1.f;  // shift of the maximum, factor of the sums
             if (seen && (open || x > kGrow)) {
               d = -x;
               f = open ? 0.f : exp2f(-x);
             }
-            if (mine) {
-              nm[st0 + c] += d;
-              fd[st0 + c] = d;
-              fl[st0 + c] = f;
-              fo[st0 + c] = f * fv;
-            }
+            nm[st0 + c] += d;
+            fd[st0 + c] = d;
+            fl[st0 + c] = f;
+            fo[st0 + c] = f * fv;
             const unsigned sn = __ballot_sync(0xffffffffu, seen);
             if (lane == 0) unset_s[g * C::NB + n] = unset[n] & ~sn;
           }
@@ -712,8 +702,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
       float a[C::BS];
 #pragma unroll
       for (int c = 0; c < C::BS; ++c) a[c] = lacc[n * C::BS + c];
-      const float ls = col_reduce<C::BS>(a, lane, [](float x, float z) { return x + z; });
-      if (lane < C::BS) red[(g * 4 + qd) * C::CP + n * C::BS + lane] = ls;
+      const float ls = col_reduce(a, lane, [](float x, float z) { return x + z; });
+      red[(g * 4 + qd) * C::CP + n * C::BS + lane] = ls;
     }
     if (qd == 0 && lane == 0) {
       vref_s[g] = vref;

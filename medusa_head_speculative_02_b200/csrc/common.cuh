@@ -363,35 +363,6 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
-// Warp-collective: 128 consecutive fp32 columns, two loads in flight, one wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
-#define MEDUSA_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
-                     "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-#define MEDUSA_R64(i) MEDUSA_R8(i), MEDUSA_R8(i + 8), MEDUSA_R8(i + 16), MEDUSA_R8(i + 24), \
-                      MEDUSA_R8(i + 32), MEDUSA_R8(i + 40), MEDUSA_R8(i + 48), MEDUSA_R8(i + 56)
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
-      "}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
-      "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
-      "}, [%129];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : MEDUSA_R64(0), MEDUSA_R64(64)
-      : "r"(taddr), "r"(taddr + 64u)
-      : "memory");
-#undef MEDUSA_R64
-#undef MEDUSA_R8
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
-}
 // Warp-collective store of 32 32-bit columns to this warp's TMEM lanes, plus
 // its completion wait.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -524,11 +495,6 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // 2^x on the FMA/ALU pipes (offloads the MUFU unit), two lanes at a time
 // in packed fp32x2 arithmetic: Cody-Waite split x = n + f with n = round(x),
 // obtained by adding 1.5 * 2^23, and f in [-0.5, 0.5]; 2^f by the degree-3
@@ -623,10 +589,11 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 // Programmatic dependent launch: wait until every kernel this one depends on
-// has completed and its memory is visible (a kernel must not take data that
-// another one writes as `const T* __restrict__` or through __ldg: such loads
-// count as constant for the whole kernel and were moved ahead of this wait); let the next kernel in the stream
+// has completed and its memory is visible; let the next kernel in the stream
 // be scheduled (it still waits in its own griddepcontrol.wait).
+// A kernel must not take data that another one writes as `const T*
+// __restrict__` or through __ldg: such loads count as constant for the whole
+// kernel and were moved ahead of the wait.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
