@@ -445,8 +445,12 @@ class PackedCache:
     the caller's tensors; ``PackedCache.empty`` makes zeroed ones (every row
     then stands for zeros)."""
 
-    __slots__ = ("k_codes", "k_par", "v_codes", "v_par", "layers", "B", "Hkv", "Lcap", "dh",
-                 "device", "_idx", "_ptrs")
+    __slots__ = ("_t", "layers", "B", "Hkv", "Lcap", "dh", "device", "_idx", "_ptrs")
+    # read-only: the calls use the pointers taken (and checked) at construction
+    k_codes = property(lambda self: self._t[0])
+    k_par = property(lambda self: self._t[1])
+    v_codes = property(lambda self: self._t[2])
+    v_par = property(lambda self: self._t[3])
 
     def __init__(self, k_codes, k_par, v_codes, v_par):
         _need(k_codes, "k_codes", torch.uint8)
@@ -458,7 +462,7 @@ class PackedCache:
         self._ptrs = (k_codes.data_ptr(), _chk(k_par, "k_par", torch.bfloat16, par, dev),
                       _chk(v_codes, "v_codes", torch.uint8, shape, dev),
                       _chk(v_par, "v_par", torch.bfloat16, par, dev))
-        self.k_codes, self.k_par, self.v_codes, self.v_par = k_codes, k_par, v_codes, v_par
+        self._t = (k_codes, k_par, v_codes, v_par)
         self.layers = shape[0] if len(shape) == 5 else None
         self.B, self.Hkv, self.Lcap = shape[-4:-1]
         self.dh = 2 * shape[-1]
@@ -549,6 +553,8 @@ def _ext_buffers(size, q, tree, Hkv, Lcap, window, sinks, dev, out, ws):
     B, N, Hq, dh = q.shape
     if N != tree.N:
         raise ValueError(f"q has {N} nodes, tree has {tree.N}")
+    if not (0 <= window < 2**31 and 0 <= sinks < 2**31):  # (a C int would wrap)
+        raise ValueError(f"window and sinks must be in [0, 2^31), got {window} and {sinks}")
     if out is None:
         out = torch.empty_like(q)
     else:

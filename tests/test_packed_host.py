@@ -23,9 +23,9 @@ def _unpack(B=1, T=4, H=2, dh=128, Lcap=8, dt=L.BF16, out=P, kc=P):
     return L.lib().medusa_kv_unpack(kc, P, P, P, P, None, B, T, H, dh, Lcap, dt, P, out, None)
 
 
-def _compact(B=1, H=2, dh=128, Lcap=8, K=4, layers=1, kc=P, alen=P):
+def _compact(B=1, H=2, dh=128, Lcap=8, K=4, layers=1, kc=P, alen=P, new_len=None):
     return L.lib().medusa_kv_compact_packed(kc, P, P, P, layers, P, alen, P, B, H, dh, Lcap, K,
-                                            None, None)
+                                            new_len, None)
 
 
 @pytest.mark.parametrize("fn", [_pack, _unpack])
@@ -59,6 +59,9 @@ def test_compact_refusals():
     assert _compact(Lcap=6) == L.ERR_UNSUPPORTED
     assert _compact(alen=None) == L.ERR_INVALID_ARG
     assert _compact(kc=ODD) == L.ERR_INVALID_ARG
+    assert _compact(new_len=P) == L.ERR_INVALID_ARG       # the lengths themselves
+    assert b"new_len" in L.lib().medusa_last_error()
+    assert _compact(alen=ODD, new_len=ODD) == L.ERR_INVALID_ARG
     assert _compact(B=0) == L.OK and _compact(layers=0) == L.OK
 
 
