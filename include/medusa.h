@@ -417,7 +417,7 @@ int medusa_tree_attention_window(const void* q, const void* k_cache, const void*
  *   code = clamp(rint(x / scale) + zero, 0, 15),
  * each step in fp32, rounded to nearest, rint with ties to even; it stands
  * for scale * (code - zero).  A row of zeros has scale 0.  A row with a NaN,
- * an infinity or a range above the largest bf16 gets scale NaN.
+ * an infinity or a range hi - lo beyond fp32 gets scale NaN.
  * Layout, all 16-byte aligned:
  *   *_codes [B][Hkv][Lcap][dh/2] bytes, element 2i in the low half of byte i;
  *   *_par   [B][Hkv][Lcap][2] bf16: (scale, zero).
@@ -428,7 +428,8 @@ int medusa_tree_attention_window(const void* q, const void* k_cache, const void*
  * Stores the rows of new tokens: k, v [B][T][Hkv][dh] of dtype; token t <
  * count[b] of sequence b goes to slot start[b] + t.  count [B] int32 or NULL
  * (= T).  Tokens past the count and slots outside [0, Lcap) are skipped:
- * what the cache holds there stays.  start [B] int32.
+ * what the cache holds there stays.  start [B] int32.  T * Hkv < 2^31 - 1024
+ * (else UNSUPPORTED; the same for medusa_kv_unpack).
  */
 int medusa_kv_pack(const void* k, const void* v, int dtype, const int32_t* start,
                    const int32_t* count, int B, int T, int Hkv, int dh, int Lcap, void* k_codes,
@@ -447,7 +448,8 @@ int medusa_kv_unpack(const void* k_codes, const void* k_par, const void* v_codes
  * medusa_kv_compact on the 4-bit caches of n_layers layers, one launch.  The
  * layers' arrays follow one another: *_codes [n_layers][B][Hkv][Lcap][dh/2],
  * *_par [n_layers][B][Hkv][Lcap][2].  Rows move bit for bit; new_len [B] (may
- * be NULL) as medusa_kv_compact writes it; same skipped entries.
+ * be NULL; an array of its own, not prefix_len or accept_len) as
+ * medusa_kv_compact writes it; same skipped entries.
  */
 int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_par, int n_layers,
                              const int32_t* prefix_len, const int32_t* accept_len,
@@ -458,11 +460,27 @@ int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_
  * Tree attention over the 4-bit cache: medusa_tree_attention_window (window =
  * 0: medusa_tree_attention) with k_j and v_j the values the rows stand for.
  * q, out [B][N][Hq][dh] of dtype; a tree of one node (N = 1) is plain
- * single-token decoding.  bf16 with dh = 128 runs on a tcgen05 kernel (any
- * Hq/Hkv), which holds the codes exactly (fp16 code - zero), the softmax
- * statistics in fp32 and the weights rounded once to fp16; other shapes on a
- * SIMT kernel in fp32.  A visible row with scale NaN makes its node's output
- * NaN; slots that no node sees may hold anything.  q finite.
+ * single-token decoding.  Only the key tiles with a visible slot are read.
+ * A visible row with scale NaN makes the output of the nodes that see it NaN;
+ * slots that no node sees may hold anything.  A sequence with L_b < 0 or
+ * L_b + N > Lcap gets rows of zeros.  q finite.
+ * bf16 with dh = 128 runs on the tensor cores, by the query rows per kv-head
+ * R = N Hq/Hkv (any Hq/Hkv):
+ *   R <= 16   mma.sync, a warp per 16-key group; codes exact in fp16
+ *   R <= 128  tcgen05, keys as the MMA's rows; codes exact in fp16
+ *   else      tcgen05, query rows as the MMA's rows; K and V rows times their
+ *             scale rounded once to fp16
+ * Scores, softmax statistics, sums and products are fp32.  Softmax weights
+ * (in the first two kernels times the value scale) are rounded once to fp16,
+ * relative to the row's maximum (and to the largest value scale): below 2^-21
+ * they lose bits, below 2^-32 they count as 0.  In the last kernel so do K and
+ * V rows whose scale is below 2^-20 of the largest of their 128 keys (K) or of
+ * the keys so far (V).  Queries are held in fp16 under one power of two for at
+ * most 256 query rows of a kv-head: elements below 2^-26 of the largest lose
+ * bits.  |q| and the row scales stay below 2^100.
+ * fp32, and dh = 64, run on a SIMT kernel in fp32.
+ * Workspace: the size its own query gives (it depends on window and sinks),
+ * 16-byte aligned.
  */
 size_t medusa_tree_attention_packed_workspace_size(const medusa_tree_t* tree, int B, int Hq,
                                                    int Hkv, int dh, int Lcap, int dtype,

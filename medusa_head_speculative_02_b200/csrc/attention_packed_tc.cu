@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   __syncthreads();  // qmax
   // Q: a warp per query row, a lane 4 dims; the largest |q| of the CTA's rows
   // sets one power-of-two factor (fp16 then holds every bf16 value down to
-  // 2^-28 of it exactly)
+  // 2^-26 of it exactly, the odd pairs' 1/16 included)
   constexpr int RPW = (NC + kWarps - 1) / kWarps;
   uint2 qv[RPW];
   float qm = 0.f;
