@@ -34,13 +34,19 @@
 // What bounds it (64-node trees): the chain products -> softmax -> products of
 // a tile, and per tile and softmax thread the 16 to 64 rows' multiply-add,
 // exponential and rounding.  64 rows, 37 heads x 4 sequences of 8K: 104 us;
-// 64 rows, 32 heads, 2K prefix (the 7B verify step): 23.6 us with the merge,
-// launch to launch, against a cache of 1.6 us of HBM time.
+// 64 rows, 32 heads, 2K prefix (the 7B verify step): 21.1 us launch to launch,
+// against a cache of 1.6 us of HBM time.
+//
+// Key chunks fill the GPU when there are few (sequence, kv-head) pairs; up to 8
+// of them form a cluster and merge through distributed shared memory when all
+// clusters run at once (7B: 23.6 us with partial rows in the workspace and a
+// second kernel).
 //
 // TMEM: O^T, two S^T buffers, two K buffers.
 // This source is compiled without relocatable device code: register splits
 // between warpgroups (setmaxnreg) are only honoured then, and without them the
 // softmax threads' 64 rows would spill.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -51,8 +57,10 @@
 #include "visible.cuh"
 
 namespace medusa {
+namespace cg = cooperative_groups;
 namespace {
 
+constexpr int kMaxClusterChunks = 8;  // portable cluster size
 constexpr int BK = 128;   // keys per tile
 constexpr int DH = 128;
 constexpr uint32_t kCodeTile = BK * DH / 2;   // 8 KB
@@ -95,6 +103,10 @@ struct Cfg {
                                     2 * (4 * 4 + NB * 4 + 4) + (NC / BS) * (MEDUSA_MAX_K + 2) * 4;
   static constexpr size_t kSmem = 1024 + oMisc + kMisc;
   static constexpr uint32_t kTmemCols = NC <= 32 ? 256 : 512;  // O (per set) | S S | K K
+  // fused merge: partial rows [NC][kOS] fp32 and their (maximum, sum), over V and P^T
+  static constexpr int kOS = DH + 4;
+  static constexpr uint32_t oMl = oV + NC * kOS * 4;
+  static_assert(oMl + NC * 8 <= oCode, "partial rows");
   static constexpr uint32_t tS = kSets * NC;
   static constexpr uint32_t tK = tS + 2 * NC;
   static_assert(tK + 2 * 64 <= kTmemCols, "TMEM columns");
@@ -109,6 +121,7 @@ struct PackedParams {
   const int32_t* depth;
   const int32_t* parent;
   int B, N, W, K, Hq, Hkv, G, Lcap, R, groups, P, window, sinks;
+  int fuse;      // key-major: the P chunks are a cluster and merge in it
   float scale2;  // softmax scale * log2(e)
   __nv_bfloat16* out;
   float* po;
@@ -173,6 +186,57 @@ __device__ __forceinline__ Tiles tile_list(int Lb, int N, int window, int sinks)
   return t;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Merge of the P chunks of a (sequence, kv-head) by the cluster they form,
+// between two cluster_sync of every thread: rank c takes rows [c per, (c + 1)
+// per), one of `warps` warps a row, from every rank's shared memory.
+template <int NC>
+__device__ __forceinline__ void merge_chunks(uint8_t* sm, int rank, int b, int kvh, int warp, int warps,
+                                             const PackedParams& p) {
+  using C = Cfg<NC>;
+  cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  const int per = (p.R + p.P - 1) / p.P;
+  const int r1 = min(p.R, (rank + 1) * per);
+  for (int r = rank * per + warp; r < r1; r += warps) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < p.P) ml = cl.map_shared_rank(reinterpret_cast<float2*>(sm + C::oMl), lane)[r];
+    float M = ml.x;
+#pragma unroll
+    for (int o = kMaxClusterChunks / 2; o > 0; o >>= 1)
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = __shfl_sync(0xffffffffu, M, 0);
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    float Ls = w == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+    for (int o = kMaxClusterChunks / 2; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+    Ls = __shfl_sync(0xffffffffu, Ls, 0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < p.P; ++c) {
+      const float wc = __shfl_sync(0xffffffffu, w, c);
+      if (wc == 0.f) continue;
+      const float4 o = reinterpret_cast<const float4*>(
+          cl.map_shared_rank(reinterpret_cast<float*>(sm + C::oV), c) + (size_t)r * C::kOS)[lane];
+      acc.x = fmaf(wc, o.x, acc.x);
+      acc.y = fmaf(wc, o.y, acc.y);
+      acc.z = fmaf(wc, o.z, acc.z);
+      acc.w = fmaf(wc, o.w, acc.w);
+    }
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+    const int node = r / p.G, g = r - node * p.G;
+    __nv_bfloat16* dst =
+        p.out + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH + 4 * lane;
+    __align__(8) __nv_bfloat162 h[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                                        __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(h);
+  }
+}
+
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     tree_attn_packed_kernel(const __grid_constant__ CUtensorMap tmKc,
@@ -235,12 +299,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   }
   griddep_wait();  // prefix lengths, queries and the cache may come from the kernel ahead
 
-  const int id = blockIdx.x;
-  const int grp = id % p.groups;
-  const int chunk = (id / p.groups) % p.P;
-  const int bk = id / p.groups / p.P;
+  const int chunk = blockIdx.x % p.P;  // (fused: the rank in the cluster)
+  const int bk = blockIdx.x / p.P;
   const int b = bk / p.Hkv, kvh = bk - b * p.Hkv;
-  const int row0 = grp * NC;
   const int Lb = p.L[b];
   const bool seq_ok = Lb >= 0 && (long long)Lb + p.N <= p.Lcap;
   Tiles tl{0, 0, 0};
@@ -250,9 +311,15 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
 
   if (T == 0) {  // no key in this chunk
     griddep_launch_dependents();
-    for (int e = threadIdx.x; e < NC; e += C::kThreads) {
-      const int r = row0 + e;
-      if (r >= p.R) continue;
+    if (p.fuse) {
+      if (threadIdx.x < NC)
+        reinterpret_cast<float2*>(sm + C::oMl)[threadIdx.x] = make_float2(-INFINITY, 0.f);
+      cluster_sync();
+      merge_chunks<NC>(sm, chunk, b, kvh, warp, kWarps, p);
+      cluster_sync();
+      return;
+    }
+    for (int r = threadIdx.x; r < p.R; r += C::kThreads) {
       if (p.P > 1) {
         p.pml[((size_t)bk * p.P + chunk) * p.R + r] = make_float2(-INFINITY, 0.f);
       } else {
@@ -289,9 +356,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   float qm = 0.f;
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
-    const int c = warp + i * kWarps, r = row0 + c;
+    const int r = warp + i * kWarps;
     qv[i] = make_uint2(0u, 0u);
-    if (c < NC && r < p.R) {
+    if (r < p.R) {
       const int node = r / p.G, g = r - node * p.G;
       qv[i] = reinterpret_cast<const uint2*>(
           p.q + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH)[lane];
@@ -311,10 +378,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
   }
   for (int c = threadIdx.x; c < NC; c += C::kThreads) {
-    const int r = row0 + c, node = min(r / p.G, p.N - 1);
+    const int node = min(c / p.G, p.N - 1);
     cnode[c] = node;
     cdepth[c] = p.depth[node];
-    crow[c] = r < p.R ? node * p.Hq + kvh * p.G + (r - node * p.G) : -1;
+    crow[c] = c < p.R ? node * p.Hq + kvh * p.G + (c - node * p.G) : -1;
   }
   for (int c = threadIdx.x; c < C::kState; c += C::kThreads) nm[c] = 0.f;
   tc_fence_before();
@@ -742,8 +809,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         const int gs = C::kSets == 2 ? s : g;
         fo[s * NC + c] = w[s] * inv * vref_s[gs];
       }
-      if (p.P > 1 && crow[c] >= 0)
-        p.pml[((size_t)bk * p.P + chunk) * p.R + row0 + c] = make_float2(M, Ls);
+      if (p.fuse)
+        reinterpret_cast<float2*>(sm + C::oMl)[c] = make_float2(M, Ls);
+      else if (p.P > 1 && crow[c] >= 0)
+        p.pml[((size_t)bk * p.P + chunk) * p.R + c] = make_float2(M, Ls);
     }
     named_bar_sync(bar_id, 128);
     if (!bad) {
@@ -753,10 +822,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
       const int dim = (key & ~7) + jj + 4 * (key & 1);
       const float unit = (jj & 1) ? 0x1p13f : 0x1p17f;  // 2^20 or 2^24, times 2^-7
       __nv_bfloat16* ob = p.out + (size_t)b * p.N * p.Hq * DH + dim;
-      float* pb = p.po + (((size_t)bk * p.P + chunk) * p.R + row0) * DH + dim;
+      float* pb = p.po + ((size_t)bk * p.P + chunk) * p.R * DH + dim;
+      float* sb = reinterpret_cast<float*>(sm + C::oV) + dim;
 #pragma unroll 1
       for (int c0 = e0; c0 < e0 + EC; c0 += 8) {
-        if (row0 + c0 >= p.R) break;  // warp-uniform
+        if (c0 >= p.R) break;  // warp-uniform
         float o8[8], x8[8];
         tmem_ld8(tmem + lane_base + (uint32_t)c0, o8);
         if constexpr (C::kSets == 2) tmem_ld8(tmem + lane_base + (uint32_t)(NC + c0), x8);
@@ -769,10 +839,21 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
           if constexpr (C::kSets == 2)
             o += fo[NC + c0 + e] == 0.f ? 0.f : x8[e] * unit * fo[NC + c0 + e];
           if (p.P == 1) ob[(size_t)r * DH] = __float2bfloat16_rn(o);
+          else if (p.fuse) sb[(c0 + e) * C::kOS] = o;
           else pb[(size_t)(c0 + e) * DH] = o;
         }
       }
     }
+    if (p.fuse) {
+      cluster_sync();
+      // (the softmax warps: the others have too few registers left)
+      merge_chunks<NC>(sm, chunk, b, kvh, warp - 4 * (1 + C::kUnpackWgs), 8, p);
+      cluster_sync();
+    }
+  }
+  if (wg <= C::kUnpackWgs && p.fuse) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -788,9 +869,44 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
 
 struct PackedPlan {
   int NC, R, groups, P;  // NC = 256: two query tiles a CTA (attention_packed_pair.cuh)
+  bool fuse;             // chunks merge in a cluster
   long long ctas;
   size_t off_o, off_ml, total;
 };
+
+template <int NC>
+int max_active_clusters(int P) {
+  static std::atomic<bool> done[64];
+  static std::atomic<int> cache[64][kMaxClusterChunks + 1];
+  using C = Cfg<NC>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  const int v = cache[dev][P].load(std::memory_order_relaxed);
+  if (v) return v - 1;
+  if (ensure_max_smem(tree_attn_packed_kernel<NC>, (int)C::kSmem, done,
+                      "cudaFuncSetAttribute(tree_attn_packed_kernel)"))
+    return 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, tree_attn_packed_kernel<NC>, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // not an error of the caller's stream: no in-cluster merge
+    return 0;
+  }
+  cache[dev][P].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
 
 PackedPlan packed_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, int window,
                        int sinks) {
@@ -813,8 +929,16 @@ PackedPlan packed_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, i
     }
   }
   p.ctas = units * p.P;
+  // chunks merge in a cluster when every cluster runs at once
+  p.fuse = false;
+  if (p.NC <= 128 && p.P > 1 && p.P <= kMaxClusterChunks) {
+    const int n = p.NC == 32   ? max_active_clusters<32>(p.P)
+                  : p.NC == 64 ? max_active_clusters<64>(p.P)
+                               : max_active_clusters<128>(p.P);
+    p.fuse = units <= n;
+  }
   WsCarver w;
-  const size_t rows = p.P > 1 ? (size_t)B * Hkv * p.P * p.R : 0;
+  const size_t rows = p.P > 1 && !p.fuse ? (size_t)B * Hkv * p.P * p.R : 0;
   p.off_o = w.take<float>(rows * DH);
   p.off_ml = w.take<float2>(rows);
   p.total = w.total();
@@ -829,8 +953,20 @@ int packed_run(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& 
   int rc = ensure_max_smem(tree_attn_packed_kernel<NC>, (int)C::kSmem, done,
                            "cudaFuncSetAttribute(tree_attn_packed_kernel)");
   if (rc) return rc;
-  cudaError_t e = launch_pdl(tree_attn_packed_kernel<NC>, dim3((unsigned)ctas), dim3(C::kThreads),
-                             C::kSmem, st, kc, vc, kp, vp, p);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.P;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.fuse ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_packed_kernel<NC>, kc, vc, kp, vp, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "tree_attn_packed_kernel launch");
 }
@@ -912,6 +1048,7 @@ int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStre
   p.R = pl.R;
   p.groups = pl.groups;
   p.P = pl.P;
+  p.fuse = pl.fuse ? 1 : 0;
   p.window = a.window;
   p.sinks = a.sinks;
   p.scale2 = a.scale * 1.4426950408889634f;
@@ -925,7 +1062,7 @@ int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStre
     case 128: rc = packed_run<128>(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
     default: rc = pair_run(mKc, mVc, mKp, mVp, p, pl.ctas, st); break;
   }
-  if (rc || pl.P == 1) return rc;
+  if (rc || pl.P == 1 || pl.fuse) return rc;
   return attention_combine_launch(a, p.po, p.pml, pl.P, st);
 }
 
