@@ -22,7 +22,7 @@
 // A row is taken by dh/8 lanes of a warp, 8 values (one 32-bit code word) each,
 // so loads of values are 16 or 32 bytes per lane and coalesced along the
 // heads.  The read back is bound by HBM (16 ragged prompts of up to 8192
-// tokens, 8 heads of 128 in bf16: 138 us), the store by instruction issue (181
+// tokens, 8 heads of 128 in bf16: 132 us), the store by instruction issue (118
 // us, see row_grid), both and the compaction by launch latency at a tree's
 // few rows.
 #include "common.cuh"
@@ -33,21 +33,78 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 consecutive values of a row as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 8 consecutive values of a row as loaded, and as four fp32 pairs.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float x[8];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
   }
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ float get(int i) const { return x[i]; }
+  // min(0, min x) and max(0, max x) over the row's LPR lanes; hi is infinite
+  // or NaN if a value is
+  template <int LPR>
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    float nan = 0.f;
+    lo = hi = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      nan = fmaf(x[i], 0.f, nan);  // NaN from a NaN or an infinity
+    }
+    if (nan != 0.f) hi = INFINITY;  // reaches every lane through the row maximum
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+  }
+};
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  // in pairs, exact in bf16: (lo, -hi) in one register, so a step over the
+  // lanes is one shuffle and one minimum
+  template <int LPR>
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    const uint32_t mn = min_nan2(min_nan2(w[0], w[1]), min_nan2(w[2], w[3]));
+    const uint32_t mx = max_nan2(max_nan2(w[0], w[1]), max_nan2(w[2], w[3]));
+    uint32_t m = min_nan2(__byte_perm(mn, mx, 0x5410) ^ 0x80000000u,
+                          __byte_perm(mn, mx, 0x7632) ^ 0x80000000u);
+    m = min_nan2(m, 0u);
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) m = min_nan2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    lo = __uint_as_float(m << 16);
+    hi = -__uint_as_float(m & 0xffff0000u);
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -60,11 +117,12 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
 }
 
 // The codes of 8 values, divided: rint of the correctly rounded quotients.
-__device__ __forceinline__ uint32_t codes_by_division(const float (&x)[8], float s, float zero) {
+template <typename T>
+__device__ __forceinline__ uint32_t codes_by_division(const Raw8<T>& x, float s, float zero) {
   uint32_t w = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + zero, 0.f), 15.f);
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(x.get(i), s)) + zero, 0.f), 15.f);
     w |= (uint32_t)(int)c << (4 * i);
   }
   return w;
@@ -73,28 +131,26 @@ __device__ __forceinline__ uint32_t codes_by_division(const float (&x)[8], float
 // Encodes one row held 8 values to a lane by LPR neighbouring lanes: this
 // lane's code word, and the row's (scale, zero) word.
 //
-// rint(x / s): x times the hardware's 1 / s (1 ulp) is within 4e-6 of the
-// quotient (|x / s| < 16), so its nearest integer is the quotient's unless it
-// lies that close to a tie; only a lane with such a value divides (a lane in
-// 3000).  Adding 1.5 * 2^23 rounds to nearest even and leaves the integer in
-// the low bits, so no conversion instruction is used (rint and float-to-int run
-// at an eighth of the rate of an addition).  A code is never negative: rint is
-// odd and monotone, so rint(x / s) >= rint(lo / s) = -zero.
-template <int LPR>
-__device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
-  float lo = 0.f, hi = 0.f, nan = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    nan = fmaf(x[i], 0.f, nan);  // NaN from a NaN or an infinity
-  }
-  if (nan != 0.f) hi = INFINITY;  // reaches every lane through the row maximum
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
+// rint(x / s) without a division: x times the hardware's 1 / s (1 ulp) is
+// within 4e-6 of the quotient (|x / s| < 16).
+//   bf16: x and s have 8 significant bits, so a quotient that is no tie is at
+//   least 1/512 away from one.  Adding 1.5 * 2^13 rounds to the nearest
+//   multiple of 2^-10: ties come out exact, the others stay on their side.
+//   (One value in 400 is a tie: testing for them and dividing there cost 4
+//   warps in 10 eight divisions.)
+//   fp32: the nearest integer of the product is the quotient's unless it lies
+//   that close to a tie; a lane with such a value (one in 6000) divides.
+// Adding 1.5 * 2^23 rounds to nearest even and leaves the integer in the low
+// bits, so no conversion instruction is used (rint and float-to-int run at an
+// eighth of the rate of an addition); the eight integers go into the word by
+// shifts and additions, the offsets of all by one multiply-add.  A code is
+// never negative: rint is odd and monotone, so rint(x / s) >= rint(lo / s) =
+// -zero.  It is 16 at most, and clamped, in a row whose lo and hi both round
+// away from 0 (one in 90).
+template <typename T, int LPR>
+__device__ __forceinline__ uint32_t encode(const Raw8<T>& x, uint32_t& par) {
+  float lo, hi;
+  x.template range<LPR>(lo, hi);
   const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
   const float s = __bfloat162float(sb);
   if (!(s <= 3.4028234e38f)) {
@@ -107,22 +163,49 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[8], uint32_t& par) {
   }
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  const float qz = -lo * r, tz = __fadd_rn(qz, kMagic);
-  float far = fabsf(qz - __fsub_rn(tz, kMagic));  // largest distance from an integer
-  const int zi = __float_as_int(tz) - 0x4b400000;
-  const int bias = zi - 0x4b400000;
-  uint32_t w = 0u;
-#pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float q = x[i] * r;
-    const float t = __fadd_rn(q, kMagic);
-    far = fmaxf(far, fabsf(q - __fsub_rn(t, kMagic)));
-    w = w * 16u + (uint32_t)__viaddmin_s32(__float_as_int(t), bias, 15);
+  constexpr bool kFine = sizeof(T) == 2;  // ties made exact
+  constexpr float kMagic = 12582912.f;    // 1.5 * 2^23
+  constexpr float kFirst = kFine ? 12288.f : kMagic;  // 1.5 * 2^13
+  constexpr int kBits = 0x4b400000;       // kMagic's bits: those of kMagic + n are kBits + n
+  float tz = fmaf(-lo, r, kFirst), th = fmaf(hi, r, kFirst);
+  if (kFine) {
+    tz = __fadd_rn(tz, kMagic - kFirst);
+    th = __fadd_rn(th, kMagic - kFirst);
   }
   float zero = __fsub_rn(tz, kMagic);
-  // (far is the lane's own: every lane of a row finds the same zero either way)
-  if (!(far <= 0.49999f) || s < 1e-30f) {  // (1 / s may overflow for the smallest scales)
+  float far = fabsf(fmaf(-lo, r, -zero));  // fp32: largest distance from an integer
+  const int bias = __float_as_int(tz) - 2 * kBits;
+  const bool over = __float_as_int(th) + bias > 15;
+  const unsigned long long r2 = f2_pack(r, r), first2 = f2_pack(kFirst, kFirst);
+  int t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long x2 = f2_pack(x.get(2 * i), x.get(2 * i + 1));
+    unsigned long long t2 = f2_fma(x2, r2, first2);
+    if (kFine) {
+      t2 = f2_add(t2, f2_pack(kMagic - kFirst, kMagic - kFirst));
+    } else {
+      float d0, d1;
+      f2_unpack(f2_fma(x2, r2, f2_fma(t2, f2_pack(-1.f, -1.f), first2)), d0, d1);
+      far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
+    }
+    float t0, t1;
+    f2_unpack(t2, t0, t1);
+    t[2 * i] = __float_as_int(t0);
+    t[2 * i + 1] = __float_as_int(t1);
+  }
+  uint32_t w = 0u;
+  if (!over) {
+#pragma unroll
+    for (int i = 7; i >= 0; --i) w = w * 16u + (uint32_t)t[i];
+    w += (uint32_t)bias * 0x11111111u;
+  } else {
+#pragma unroll
+    for (int i = 7; i >= 0; --i) w = w * 16u + (uint32_t)__viaddmin_s32(t[i], bias, 15);
+  }
+  // (1 / s may overflow for the smallest scales; far is the lane's own: every
+  // lane of a row finds the same zero either way)
+  if ((!kFine && !(far <= 0.49999f)) || s < 1e-30f) {
     zero = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f);
     w = codes_by_division(x, s, zero);
   }
@@ -150,18 +233,29 @@ struct RowGrid {
   const int32_t* count;
   int B, T, H, Lcap;
   uint32_t rows, hmul;  // T * H, floor(2^32 / H)
+  uint32_t dt, dh;      // a step of one block's rows in (token, head)
 };
 
-// Cache row of row `row` of sequence b, or -1: not one of its tokens, or
-// outside the cache.
-__device__ __forceinline__ long long cache_row(const RowGrid& g, int b, int start, int count,
-                                               uint32_t row) {
-  if (row >= g.rows) return -1;
-  const uint32_t t = fast_div(row, g.H, g.hmul);
-  const int h = (int)(row - t * g.H);
-  const long long slot = (long long)start + t;
-  if ((long long)t >= count || slot < 0 || slot >= g.Lcap) return -1;
-  return ((long long)b * g.H + h) * g.Lcap + slot;
+// Cache rows of rows `row`, `row` + one block's rows, ... of sequence b; -1: not
+// one of its tokens, or outside the cache.
+template <int RPT>
+__device__ __forceinline__ void cache_rows(const RowGrid& g, int b, int start, int count, uint32_t row,
+                                           long long (&out)[RPT]) {
+  uint32_t t = fast_div(row, g.H, g.hmul), h = row - t * g.H;
+  const uint32_t n = (uint32_t)min(count, g.T);
+  const long long base = (long long)b * g.H * g.Lcap;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const long long slot = (long long)start + t;
+    const bool in = t < n && slot >= 0 && slot < g.Lcap;
+    out[i] = in ? base + (long long)h * g.Lcap + slot : -1;
+    t += g.dt;
+    h += g.dh;
+    if (h >= (uint32_t)g.H) {
+      h -= g.H;
+      ++t;
+    }
+  }
 }
 
 template <typename T, int DH, int RPT>
@@ -180,20 +274,20 @@ __global__ void __launch_bounds__(kThreads, 4)
   for (int b = blockIdx.y; b < g.B; b += gridDim.y) {
     const int count = g.count ? g.count[b] : g.T, start = g.start[b];
     if (count <= 0 || (long long)first >= (long long)count * g.H) continue;  // (uniform) past its tokens
-    float x[RPT][8];
+    Raw8<T> x[RPT];
     long long dst[RPT];
+    const uint32_t row = first + threadIdx.x / LPR;
+    cache_rows<RPT>(g, b, start, count, row, dst);
+    const T* from = src + ((size_t)b * g.rows + row) * DH + sub * 8;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const uint32_t row = first + threadIdx.x / LPR + i * GROUPS;
-      dst[i] = cache_row(g, b, start, count, row);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-      if (dst[i] >= 0) load8(src + ((size_t)b * g.rows + row) * DH + sub * 8, x[i]);
+      x[i].clear();
+      if (dst[i] >= 0) x[i].load(from + i * (GROUPS * DH));
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       uint32_t p;
-      const uint32_t w = encode<LPR>(x[i], p);  // every lane: the row maxima are shuffles
+      const uint32_t w = encode<T, LPR>(x[i], p);  // every lane: the row maxima are shuffles
       if (dst[i] >= 0) {
         codes[dst[i] * LPR + sub] = w;
         if (sub == 0) par[dst[i]] = p;
@@ -220,11 +314,12 @@ __global__ void __launch_bounds__(kThreads)
     const int count = g.count ? g.count[b] : g.T, start = g.start[b];
     const uint32_t row0 = blockIdx.x * (GROUPS * RPT) + threadIdx.x / LPR;
     uint32_t w[RPT], p[RPT];
+    long long src[RPT];
+    cache_rows<RPT>(g, b, start, max(count, 0), row0, src);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const long long src = cache_row(g, b, start, count, row0 + i * GROUPS);
-      w[i] = src >= 0 ? codes[src * LPR + sub] : 0u;
-      p[i] = src >= 0 ? par[src] : 0u;
+      w[i] = src[i] >= 0 ? codes[src[i] * LPR + sub] : 0u;
+      p[i] = src[i] >= 0 ? par[src[i]] : 0u;
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -295,10 +390,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Few rows: one per lane group (latency); many: four in flight, in 64 registers
-// (16 ragged prompts of up to 8192 tokens, 8 heads: the store takes 181 us, 275
-// with the 90 registers the compiler takes unasked, 198 with two rows in
-// flight, 241 with one).  It is bound by instruction issue (about 200 per 8
-// values: the row's range and the 8 codes), the read back by HBM writes.
+// (16 ragged prompts of up to 8192 tokens, 8 heads: the store takes 118 us; when
+// it took 181, two rows in flight took 198, one 241).  It is bound by
+// instruction issue (the row's range and the 8 codes of a lane), the read back
+// by HBM writes.
 int row_grid(const PackedRows& a, int groups, bool* many, RowGrid* g, dim3* grid) {
   const long long rows = (long long)a.T * a.c.Hkv;
   if (rows > 0x7fffffffLL - 4 * kThreads)
@@ -311,6 +406,8 @@ int row_grid(const PackedRows& a, int groups, bool* many, RowGrid* g, dim3* grid
   g->H = a.c.Hkv;
   g->Lcap = a.c.Lcap;
   g->rows = (uint32_t)rows;
+  g->dt = (uint32_t)(groups / a.c.Hkv);
+  g->dh = (uint32_t)(groups % a.c.Hkv);
   g->hmul = a.c.Hkv == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (uint32_t)a.c.Hkv);
   const int per = groups * (*many ? 4 : 1);
   *grid = dim3((unsigned)((rows + per - 1) / per), (unsigned)(a.B < 65535 ? a.B : 65535), 2);

@@ -216,3 +216,32 @@ def test_empty_calls_and_a_captured_store():
     assert torch.equal(c.k_codes[:, :, 9:14].cpu(), codes.transpose(1, 2))
     par = torch.stack([scale, zero], -1).to(torch.bfloat16)
     assert torch.equal(outs[0].cpu(), R.decode(codes, par).float())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("exp", [0, -60, 100, -97])
+def test_quotients_at_and_beside_ties(dtype, exp):
+    """Values at (n + 1/2) scale, as far as the type holds them, and their
+    neighbours, for every significand of hi and several shares of lo: codes as
+    the definition's rounding to even gives them."""
+    g = torch.Generator().manual_seed(7)
+    hi = (128 + torch.arange(128, dtype=torch.float64)) * 2.0 ** (exp - 7)
+    rows = []
+    for share in (0.0, 0.3, 1.0, 2.5):
+        lo = -(hi * share).to(torch.bfloat16).double()
+        scale = ((hi - lo).float() / 15).to(torch.bfloat16).double()
+        n = torch.arange(-16, 16, dtype=torch.float64)
+        tie = ((n + 0.5) * scale[:, None]).to(dtype)
+        up = torch.nextafter(tie, torch.full_like(tie, math.inf))
+        down = torch.nextafter(tie, torch.full_like(tie, -math.inf))
+        rnd = (torch.rand(128, 30, generator=g, dtype=torch.float64) * (hi - lo)[:, None] + lo[:, None])
+        x = torch.cat([tie, up, down, rnd.to(dtype)], 1).double()
+        x = torch.minimum(torch.maximum(x, lo[:, None]), hi[:, None])
+        rows.append(torch.cat([x, lo[:, None], hi[:, None]], 1).to(dtype))
+    x = torch.stack(rows).view(4, 128, 1, 128).contiguous()
+    cache = _poisoned(4, 1, 128, 128)
+    st = torch.zeros(4, dtype=torch.int32, device=DEV)
+    want = _expect(cache, x, -x, [0] * 4, [128] * 4)
+    api.medusa_kv_pack(x.to(DEV), (-x).to(DEV), cache, st)
+    for a, w in zip((cache.k_codes, cache.k_par, cache.v_codes, cache.v_par), want):
+        assert _same(a.cpu(), w)
