@@ -193,7 +193,11 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One warp per output row (b, node, h): merge the chunks.
+// One warp per output row (b, node, h): merge the chunks.  Bound by latency: a
+// lane fetches one chunk's (maximum, sum), and the partial rows are loaded
+// eight at a time (one after the other, each behind its chunk's maximum, took
+// a trip to L2 per chunk and more).  A chunk without a visible key has no
+// partial row.
 template <typename T, int DH>
 __global__ void tree_attn_combine_kernel(const float* po,
                                          const float2* pml,
@@ -214,20 +218,39 @@ __global__ void tree_attn_combine_kernel(const float* po,
   const int r = node * G + g;
   const size_t base = ((size_t)b * Hkv + kvh) * chunks;
   float M = -INFINITY;
-  for (int c = 0; c < chunks; ++c) M = fmaxf(M, pml[(base + c) * R + r].x);
+  for (int c = lane; c < chunks; c += 32) M = fmaxf(M, pml[(base + c) * R + r].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[DH / 32];
 #pragma unroll
   for (int e = 0; e < DH / 32; ++e) acc[e] = 0.f;
   float Ls = 0.f;
   if (M != -INFINITY) {
-    for (int c = 0; c < chunks; ++c) {
-      const float2 ml = pml[(base + c) * R + r];
-      if (ml.x == -INFINITY) continue;
-      const float w = exp2f(ml.x - M);
-      Ls += w * ml.y;
-      const float* orow = po + ((base + c) * R + r) * DH;
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (c0 + lane < chunks) ml = pml[(base + c0 + lane) * R + r];
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      const unsigned seen = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+      const int n = min(32, chunks - c0);
+      for (int j0 = 0; j0 < n; j0 += 8) {
+        float v[8][DH / 32];
 #pragma unroll
-      for (int e = 0; e < DH / 32; ++e) acc[e] = fmaf(w, orow[lane + 32 * e], acc[e]);
+        for (int j = 0; j < 8; ++j) {
+          const bool in = (seen >> (j0 + j)) & 1u;
+          const float* orow = po + ((base + c0 + j0 + j) * R + r) * DH;
+#pragma unroll
+          for (int e = 0; e < DH / 32; ++e) v[j][e] = in ? orow[lane + 32 * e] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wc = __shfl_sync(0xffffffffu, w, j0 + j);
+          const float lc = __shfl_sync(0xffffffffu, ml.y, j0 + j);
+          if (!((seen >> (j0 + j)) & 1u)) continue;
+          Ls += wc * lc;
+#pragma unroll
+          for (int e = 0; e < DH / 32; ++e) acc[e] = fmaf(wc, v[j][e], acc[e]);
+        }
+      }
     }
   }
   const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
