@@ -530,13 +530,19 @@ RowsPlan rows_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, int w
   p.R = t->N * (Hq / Hkv);
   const long long units = (long long)B * Hkv;
   const long long nb = (ext_max_keys(Lcap, t->N, window, sinks) + KB - 1) / KB + (window > 0 ? 1 : 0);
-  // key chunks: least (waves of resident CTAs) x (blocks of a CTA + its start
-  // and end, about 4 blocks' time)
-  const long long slots = (p.R <= 8 ? 4LL : 3LL) * num_sms();
-  long long best = 0, P = 1;
+  // key chunks: least time of the resident CTAs, each with its start and end of
+  // about 4 blocks' time (6 with the merge), and half a chunk for the uneven
+  // end: the CTAs of an SM share it, so a part wave costs little, and the
+  // sequences' lengths are not known here.  (Whole waves and no end: 8
+  // sequences of 4K to 16K, 16 rows, 62 us instead of 54; 64 of 500 to 4096, 4
+  // rows, 71 instead of 64.)
+  const double slots = (p.R <= 8 ? 4.0 : 3.0) * num_sms();
+  double best = 0.0;
+  long long P = 1;
   for (long long x = 1; units > 0 && x <= 64 && x <= nb; ++x) {
-    const long long cost = ((units * x + slots - 1) / slots) * ((nb + x - 1) / x + 4 + (x > 1 ? 2 : 0));
-    if (best == 0 || cost < best) {
+    const double waves = (double)(units * x) / slots, T = (double)((nb + x - 1) / x);
+    const double cost = (waves > 1.0 ? waves : 1.0) * (T + (x > 1 ? 6.0 : 4.0)) + 0.5 * T;
+    if (x == 1 || cost < best) {
       best = cost;
       P = x;
     }
