@@ -24,8 +24,12 @@
 // positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9), so V's scales are one 16-byte load.
 //
 // The tcgen05 kernel reads and waits per 128-key tile in about 2000 cycles
-// whatever the number of rows; 8 KB + 8 KB of codes arrive in 750.  Bound:
-// HBM, then the integer pipe (88 logic operations per 16 keys and lane).
+// whatever the number of rows; 8 KB + 8 KB of codes arrive in 750.  Measured:
+// single tokens of 16 sequences of 32K, 8 kv-heads, 4 rows each: 147 us of 87
+// at the HBM rate; 9K to 32K: 95 of 55.  Bound: instruction issue (61 %) and the
+// integer pipe (57 %: 88 logic operations per 16 keys and lane).  Four blocks
+// per SM with up to 128 registers: five with 102 take 154 us, six (spilling)
+// 224, three 155; the scores in two chains of MMAs instead of one 150.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
