@@ -370,7 +370,7 @@ struct WindowTcPlan {
 WindowTcPlan window_tc_plan(const medusa_tree* t, int B, int Hq, int Hkv, int dh, int Lcap,
                             int window, int sinks) {
   WindowTcPlan p;
-  p.sh = attention_tc_shape(B, Hq, Hkv, t->N, window_tc_lcap(Lcap, t->N, window, sinks));
+  p.sh = attention_tc_shape(B, Hq, Hkv, t->N, window_tc_lcap(Lcap, t->N, window, sinks), true);
   WsCarver w;
   const size_t rows = p.sh.P > 1 && !p.sh.fuse ? (size_t)B * Hkv * p.sh.P * t->N * (Hq / Hkv) : 0;
   p.off_o = w.take<float>(rows * dh);

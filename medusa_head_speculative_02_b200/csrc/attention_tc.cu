@@ -52,7 +52,7 @@
 // everything between is never read.  Work per step is then bounded by the
 // window: 64-node trees, 32 heads, 2048-token prefix, window 512: 6 key tiles
 // per kv-head instead of 17 (14 us, of them 12 start-up, merge and launch); 4 x
-// 32K, 52 heads, 256-node trees, window 4096: 205 us of 75 at the HBM rate (the
+// 32K, 52 heads, 256-node trees, window 4096: 170 us of 75 at the HBM rate (the
 // whole prefix 1.0 ms), bound by the same waits as without a window; 16 single
 // tokens, 8 kv-heads, window 4095: 58 us of 41.
 #include <cooperative_groups.h>
@@ -1236,7 +1236,7 @@ int attention_tc_chunks(int B, int Hq, int Hkv, int N, int Lcap) {
   return (int)P;
 }
 
-TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap) {
+TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap, bool window) {
   TcShape sh;
   sh.P = attention_tc_chunks(B, Hq, Hkv, N, Lcap);
   sh.tiles = 1;
@@ -1258,7 +1258,14 @@ TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap) {
   // the chunks can merge in-cluster.
   const long long sms = num_sms();
   const long long T = (Lcap - N + BN - 1) / BN + (N + BN - 1) / BN;
-  const long long cost1 = ((units * sh.P + sms - 1) / sms) * ((T + sh.P - 1) / sh.P);
+  // With a window a CTA has few tiles, and its start and end count: about 8
+  // tiles' time with one query tile (14 with chunks to merge), 6.5 with two (10.5
+  // with the merge).  52 heads, 256-node trees: 2 sequences, window 1024 and
+  // 4096, 75 and 125 us without it and 43 and 102 with it; 4 sequences 112 and
+  // 199, 76 and 170.  (Counted twice below, to stay in integers.)
+  const long long end1 = !window ? 0 : sh.P > 1 ? 28 : 16;
+  const long long cost1 =
+      ((units * sh.P + sms - 1) / sms) * (2 * ((T + sh.P - 1) / sh.P) + end1);
   const long long pairs = (long long)B * Hkv * ((mtiles + 1) / 2);
   const long long max_p = ((long long)(Lcap - N) + 4 * BN - 1) / (4 * BN);  // >= 4 tiles each
   long long best = cost1 * 10;
@@ -1273,7 +1280,8 @@ TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap) {
       if (n <= 0) break;
       waves = (pairs + n - 1) / n;
     }
-    const long long cost2 = 18 * waves * ((T + P2 - 1) / P2);
+    const long long end2 = !window ? 0 : P2 > 1 ? 21 : 13;
+    const long long cost2 = 18 * waves * (2 * ((T + P2 - 1) / P2) + end2);
     if (cost2 < best) {
       best = cost2;
       bestP = P2;

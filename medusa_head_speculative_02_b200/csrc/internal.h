@@ -154,7 +154,7 @@ struct TcShape {
   int tiles;
   bool fuse;
 };
-TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap);
+TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap, bool window = false);
 int attention_tc_run(const AttnArgs& a, const TcShape& sh, float* po, float2* pml,
                      cudaStream_t st);
 
