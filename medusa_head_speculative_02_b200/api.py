@@ -445,8 +445,8 @@ class PackedCache:
     the caller's tensors; ``PackedCache.empty`` makes zeroed ones (every row
     then stands for zeros)."""
 
-    __slots__ = ("_t", "layers", "B", "Hkv", "Lcap", "dh", "device", "_idx", "_ptrs")
-    # read-only: the calls use the pointers taken (and checked) at construction
+    __slots__ = ("_t", "layers", "B", "Hkv", "Lcap", "dh", "device", "_idx")
+    # read-only: the calls rely on the shapes checked at construction
     k_codes = property(lambda self: self._t[0])
     k_par = property(lambda self: self._t[1])
     v_codes = property(lambda self: self._t[2])
@@ -459,14 +459,18 @@ class PackedCache:
             raise ValueError("k_codes must be [B][Hkv][Lcap][dh/2] or [layers][B][Hkv][Lcap][dh/2]")
         self._idx = dev = k_codes.get_device()
         par = shape[:-1] + (2,)
-        self._ptrs = (k_codes.data_ptr(), _chk(k_par, "k_par", torch.bfloat16, par, dev),
-                      _chk(v_codes, "v_codes", torch.uint8, shape, dev),
-                      _chk(v_par, "v_par", torch.bfloat16, par, dev))
+        _chk(k_par, "k_par", torch.bfloat16, par, dev)
+        _chk(v_codes, "v_codes", torch.uint8, shape, dev)
+        _chk(v_par, "v_par", torch.bfloat16, par, dev)
         self._t = (k_codes, k_par, v_codes, v_par)
         self.layers = shape[0] if len(shape) == 5 else None
         self.B, self.Hkv, self.Lcap = shape[-4:-1]
         self.dh = 2 * shape[-1]
         self.device = k_codes.device
+
+    @property
+    def _ptrs(self):
+        return [t.data_ptr() for t in self._t]
 
     @classmethod
     def empty(cls, B: int, Hkv: int, Lcap: int, dh: int, device="cuda", layers=None):

@@ -917,26 +917,29 @@ PackedPlan packed_plan(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap, i
   const long long units = (long long)B * Hkv * p.groups;
   const long long T = (ext_max_keys(Lcap, t->N, window, sinks) + BK - 1) / BK + (window > 0 ? 1 : 0);
   // key chunks: least (waves of CTAs) x (tiles of a CTA + its start and end,
-  // about 4 tiles' time)
+  // about 4 tiles' time, and the merge: 1 in a cluster, which takes every
+  // cluster running at once, 2 with a second kernel)
   const long long sms = num_sms();
   long long best = 0;
   p.P = 1;
+  p.fuse = false;
   for (long long P = 1; units > 0 && P <= 64 && P <= T; ++P) {
-    const long long cost = ((units * P + sms - 1) / sms) * ((T + P - 1) / P + 4 + (P > 1 ? 2 : 0));
+    bool fuse = false;
+    if (p.NC <= 128 && P > 1 && P <= kMaxClusterChunks && units * P <= sms) {
+      const int n = p.NC == 32   ? max_active_clusters<32>((int)P)
+                    : p.NC == 64 ? max_active_clusters<64>((int)P)
+                                 : max_active_clusters<128>((int)P);
+      fuse = units <= n;
+    }
+    const long long cost =
+        ((units * P + sms - 1) / sms) * ((T + P - 1) / P + 4 + (P == 1 ? 0 : fuse ? 1 : 2));
     if (best == 0 || cost < best) {
       best = cost;
       p.P = (int)P;
+      p.fuse = fuse;
     }
   }
   p.ctas = units * p.P;
-  // chunks merge in a cluster when every cluster runs at once
-  p.fuse = false;
-  if (p.NC <= 128 && p.P > 1 && p.P <= kMaxClusterChunks) {
-    const int n = p.NC == 32   ? max_active_clusters<32>(p.P)
-                  : p.NC == 64 ? max_active_clusters<64>(p.P)
-                               : max_active_clusters<128>(p.P);
-    p.fuse = units <= n;
-  }
   WsCarver w;
   const size_t rows = p.P > 1 && !p.fuse ? (size_t)B * Hkv * p.P * p.R : 0;
   p.off_o = w.take<float>(rows * DH);

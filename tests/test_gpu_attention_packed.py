@@ -227,3 +227,30 @@ def test_repeatable_and_captured_on_another_stream(window):
                           [41, 700], O.tree_plan(*tree), scale, window, 4)
         R.assert_close(o, *ref, BF, "fp16" if packed else "bf16")
         L.copy_(torch.tensor(Ls, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("N,Hq", [(20, 8), (64, 8), (40, 24)])  # 20, 64 and 120 rows per kv-head
+@pytest.mark.parametrize("Ls,fused", [([0, 1900, 130], True), ([5, 7900, 3000], False)])
+def test_chunk_merge_in_a_cluster_and_in_the_workspace(N, Hq, Ls, fused):
+    """Key chunks that merge in a cluster (no workspace) and, more than 8 of
+    them, in the workspace: sequences shorter than the chunks are many, and one
+    that does not fit."""
+    tree, Hkv = (5, 10, N), 8 if fused else 2
+    Hq = Hq * Hkv // 8
+    q, c, L, Lcap = _packed_inputs(3, tree, Hq, Hkv, 128, Ls, BF, spare=0)
+    t = api.Tree(*tree)
+    size = api.attention_packed_workspace_size(t, 3, Hq, Hkv, 128, Lcap, BF)
+    assert (size == 0) == fused
+    for bad in (None, 2 ** 31 - 1):
+        L2, Lb = L.clone(), list(Ls)
+        if bad is not None:
+            L2[1], Lb[1] = bad, bad
+        out, ws = Guarded(q.shape, BF, DEV), GuardedWorkspace(max(size, 1), DEV)
+        api.medusa_tree_attention_packed(q, c, L2, t, 0.088, out=out.t, ws=ws.t)
+        assert out.intact() and ws.intact()
+        ref = R.attention(q, *_values(c), Lb, O.tree_plan(*tree), 0.088, 0, 0)
+        R.assert_close(out.t, *ref, BF, "fp16")
+        first = out.t.clone()
+        for _ in range(3):
+            assert torch.equal(api.medusa_tree_attention_packed(q, c, L2, t, 0.088), first)
+    assert api.device_status() == 0

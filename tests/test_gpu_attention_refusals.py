@@ -133,3 +133,14 @@ def test_sequences_outside_the_cache(tree):
         o = c()
         assert torch.equal(o[1], g[1])
         assert not o[0].any() and not o[2].any()
+
+
+def test_cache_follows_its_tensors(tree):
+    """A tensor of the cache given other memory: the calls read the new one."""
+    q, k, v, length, cache = _inputs()
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    api.medusa_kv_pack(k, v, cache, zero)
+    want = api.medusa_tree_attention_packed(q, cache, length, tree, 0.1)
+    cache.k_codes.data, old = cache.k_codes.clone(), cache.k_codes.data
+    old.zero_()
+    assert torch.equal(api.medusa_tree_attention_packed(q, cache, length, tree, 0.1), want)
