@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import ext_reference as R
+from medusa_head_speculative_02_b200 import _lib as lib
 from medusa_head_speculative_02_b200 import api
 
 pytestmark = pytest.mark.gpu
@@ -166,6 +167,8 @@ def test_compact_moves_rows_bit_for_bit(layers, dh):
     for t, w in zip((c.k_codes, c.k_par, c.v_codes, c.v_par), arrs):
         assert torch.equal(t.cpu(), w)
     assert new.cpu().tolist() == [8, 1, 23, -1, 34, -1]
+    # the index-checked library records the bad entries (and this clears them)
+    assert api.device_status() == (lib.ERR_BOUNDS if lib.DEBUG else 0)
 
 
 def test_offsets_past_32_bits():
