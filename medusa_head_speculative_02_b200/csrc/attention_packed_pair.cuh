@@ -393,8 +393,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
         // softmax(t - 4) has read these slots: S(t - 2) followed its P(t - 3)
         if (lane == 0) sNan[(t & 3) * 4 + qd] = nan;
         if (key == 0) {
-          // Q carries 2^kexp, K 2^10 / kref
-          sScore[t & 3] = p.scale2 * ldexpf(1.f, -kexp) * (kref * 0x1p-10f);
+          // Q carries 2^kexp, K 2^10 / kref.  Never 0, which would turn the -inf
+          // of a masked score into NaN: below 2^-126 (K rows of zeros, small
+          // queries) the scores, |S| < 2^35, are 0 to fp32 with either factor
+          sScore[t & 3] = fmaxf(p.scale2 * ldexpf(1.f, -kexp) * (kref * 0x1p-10f), 0x1p-126f);
           sGrow[t & 3] = grow;
           sRef[t & 3] = vref;
         }
