@@ -117,9 +117,11 @@ __device__ __forceinline__ uint32_t row_mask(int s0, int Lb, int node, int depth
   return m;
 }
 
-// The power of two >= a scale (its bits), kept in [2^-120, 2^119].
+// The power of two >= a scale (its bits), kept in [2^-117, 2^119], where 2^10
+// over it is an fp32 number too.
+constexpr float kMinRef = 0x1p-117f;
 __device__ __forceinline__ float scale_ref(uint32_t bits) {
-  const int ex = min(246, max(7, (int)((bits >> 23) + ((bits & 0x7fffffu) ? 1 : 0))));
+  const int ex = min(246, max(10, (int)((bits >> 23) + ((bits & 0x7fffffu) ? 1 : 0))));
   return __uint_as_float((uint32_t)ex << 23);
 }
 
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
     // ---------------------------------------------------------------- unpack
     reg_dec<C::kRegsUnpack>();
     const int sw = (key >> 1) & 3;  // 64-byte swizzle of the code rows
-    float vref = 0x1p-120f;
+    float vref = kMinRef;
     bool ok = true;
     uint32_t kp = 0u, vp = 0u;
     float kref = 0.f;
@@ -550,9 +552,10 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
       ok = mbar_wait_warp(&pv_done[q], (uint32_t)(T - 1) & 1u, abort_flag);
       if (ok) {
         tc_fence_after();
-        // weights and l carry 2^7, V 2^10 / vref
-        const float vref = sRef[(T - 1) & 3] * 0x1p-10f;
-        const float f = p.P == 1 ? (l == 0.f ? 0.f : vref / l) : vref * 0x1p-7f;
+        // weights and l carry 2^7, V 2^10 / vref; the power of two comes last, as
+        // its product with 1 / l may lose bits below 2^-126
+        const float vref = sRef[(T - 1) & 3];
+        const float f = p.P == 1 ? (l == 0.f ? 0.f : 0x1p-10f / l) : 0x1p-17f;
         const int g = grow_ - node * p.G;
         __nv_bfloat16* ob =
             p.out + (((size_t)b * p.N + node) * p.Hq + (size_t)kvh * p.G + g) * DH;
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(PairCfg::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int jj = (e >> 1) & 3;
-            d[(e & 8) + jj + 4 * (e & 1)] = o16[e] * f;
+            d[(e & 8) + jj + 4 * (e & 1)] = o16[e] * f * vref;
           }
           if (p.P == 1) {
             __align__(16) __nv_bfloat162 h[8];

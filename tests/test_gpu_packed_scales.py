@@ -90,3 +90,29 @@ def test_a_nan_row_in_a_tile_of_zeros(kernel):
     rows = (~sees)[None, :, None].expand(q.shape[:3])
     got = _check(kernel, q, c, L, tree, 0.088, rows=rows)
     assert bool(got[:, sees].isnan().all())
+
+
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("exp", [110, 116, 117, 118])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_tiny_scales(kernel, exp, which):
+    """Rows whose scales are all 2^-exp, some K rows zeros; codes of V on one
+    side of zero, so that the outputs stay normal numbers of their type."""
+    q, c, L, tree = _inputs(kernel, [256, 300])
+    if which != "v":
+        c.k_par[..., 0] = 2.0 ** -exp
+        c.k_par[:, :, ::7] = 0
+    if which != "k":
+        c.v_par[..., 0] = 2.0 ** -exp
+        c.v_par[..., 1] = 0
+        c.v_codes.bitwise_or_(0x88)
+    _check(kernel, q, c, L, tree, 0.088)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_value_scales_that_start_tiny(kernel):
+    """Scales of 2^-118 in the first tiles, ordinary ones after them."""
+    q, c, L, tree = _inputs(kernel, [600, 300])
+    c.v_par[:, :, :200, 0] = 2.0 ** -118
+    c.k_par[:, :, :200, 0] = 2.0 ** -118
+    _check(kernel, q, c, L, tree, 0.088)
