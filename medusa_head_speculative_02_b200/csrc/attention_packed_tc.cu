@@ -211,15 +211,19 @@ __device__ __forceinline__ void merge_chunks(uint8_t* sm, int rank, int b, int k
     for (int o = kMaxClusterChunks / 2; o > 0; o >>= 1)
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     M = __shfl_sync(0xffffffffu, M, 0);
-    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-    float Ls = w == 0.f ? 0.f : w * ml.y;
+    // a chunk without a visible key has no row; one whose weight is 0 counts, as
+    // its sum or row may be NaN
+    const bool has = ml.x != -INFINITY;
+    const unsigned seen = __ballot_sync(0xffffffffu, has);
+    const float w = has ? exp2f(ml.x - M) : 0.f;
+    float Ls = has ? w * ml.y : 0.f;
 #pragma unroll
     for (int o = kMaxClusterChunks / 2; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
     Ls = __shfl_sync(0xffffffffu, Ls, 0);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < p.P; ++c) {
       const float wc = __shfl_sync(0xffffffffu, w, c);
-      if (wc == 0.f) continue;
+      if (!((seen >> c) & 1u)) continue;
       const float4 o = reinterpret_cast<const float4*>(
           cl.map_shared_rank(reinterpret_cast<float*>(sm + C::oV), c) + (size_t)r * C::kOS)[lane];
       acc.x = fmaf(wc, o.x, acc.x);
