@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
   // per (softmax warpgroup, row)
   float* nm = (float*)(sm + C::oMisc + 256);  // minus the row maximum (base 2)
   float* fl = nm + C::kState;                 // rescale of the sums; at the end the row sum
-  float* fo = fl + C::kState;                 // rescale of O; at the end its factor
+  float* fo = fl + C::kState;                 // rescale of O; at the end its factor (< 0: no O)
   float* fd = fo + C::kState;                 // shift of the scores
   int* cnode = (int*)(fd + C::kState);        // [NC] node of the query row
   int* cdepth = cnode + NC;                   // [NC]
@@ -805,13 +805,13 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
 #pragma unroll
       for (int s = 0; s < C::kSets; ++s) {
         w[s] = m[s] == -INFINITY ? 0.f : exp2f(m[s] - M);
-        if (w[s] != 0.f) Ls += w[s] * l[s];
+        if (m[s] != -INFINITY) Ls += w[s] * l[s];  // (a weight of 0 too: the sum may be NaN)
       }
       const float inv = p.P == 1 ? (Ls == 0.f ? 0.f : 1.f / Ls) : 1.f;
 #pragma unroll
       for (int s = 0; s < C::kSets; ++s) {
         const int gs = C::kSets == 2 ? s : g;
-        fo[s * NC + c] = w[s] * inv * vref_s[gs];
+        fo[s * NC + c] = m[s] == -INFINITY ? -1.f : w[s] * inv * vref_s[gs];
       }
       if (p.fuse)
         reinterpret_cast<float2*>(sm + C::oMl)[c] = make_float2(M, Ls);
@@ -838,10 +838,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 1)
         for (int e = 0; e < 8; ++e) {
           const int r = crow[c0 + e];
           if (r < 0) continue;
-          // a factor of 0: that warpgroup saw no key of the row (its O^T may be unwritten)
-          float o = fo[c0 + e] == 0.f ? 0.f : o8[e] * unit * fo[c0 + e];
+          // below 0: that warpgroup saw no key of the row (its O^T may be unwritten)
+          float o = fo[c0 + e] < 0.f ? 0.f : o8[e] * unit * fo[c0 + e];
           if constexpr (C::kSets == 2)
-            o += fo[NC + c0 + e] == 0.f ? 0.f : x8[e] * unit * fo[NC + c0 + e];
+            o += fo[NC + c0 + e] < 0.f ? 0.f : x8[e] * unit * fo[NC + c0 + e];
           if (p.P == 1) ob[(size_t)r * DH] = __float2bfloat16_rn(o);
           else if (p.fuse) sb[(c0 + e) * C::kOS] = o;
           else pb[(size_t)(c0 + e) * DH] = o;

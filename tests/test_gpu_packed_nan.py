@@ -14,6 +14,7 @@ BF = torch.bfloat16
 KERNELS = {
     "rows8": ((4, 3, 5), 1, 128, BF),
     "rows16": ((4, 3, 5), 3, 128, BF),
+    "keys32": ((4, 3, 9), 3, 128, BF),
     "keys64": ((5, 10, 50), 1, 128, BF),
     "keys128": ((5, 10, 50), 2, 128, BF),
     "pair": ((5, 3, 200), 1, 128, BF),
