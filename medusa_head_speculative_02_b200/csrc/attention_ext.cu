@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
       const int ri = rg + 8 * i, r = rb * RB + ri;
       const int dq = s.depth[min(r / a.G, a.N - 1)];
       float tmax = -INFINITY;
+      bool see[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int u = u0 + cg + 16 * j;
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
         } else if (vis) {
           vis = in_window(slot, Lb + dq, a.window, a.sinks);
         }
+        see[j] = vis;
         acc[i][j] = vis ? acc[i][j] : -INFINITY;
         tmax = fmaxf(tmax, acc[i][j]);
       }
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = (acc[i][j] == -INFINITY) ? 0.f : exp2f(acc[i][j] - m_new);
-        s.p[ri][cg + 16 * j] = p;
+        s.p[ri][cg + 16 * j] = see[j] ? p : -1.f;  // a negative weight: masked
         psum += p;
       }
 #pragma unroll
@@ -216,8 +218,9 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
       for (int d = 0; d < DT; ++d) o[i][d] *= corr;
     }
     __syncwarp();
-    // O: rows rg + 8 i, dims 4 cg + 64 c .. + 3; a masked key has p = 0 and
-    // its V row may hold anything, so it is skipped, not multiplied
+    // O: rows rg + 8 i, dims 4 cg + 64 c .. + 3; a masked key's V row may hold
+    // anything, so it is skipped, not multiplied (a visible one with p = 0 is
+    // not: 0 x NaN is NaN)
 #pragma unroll 1
     for (int j = 0; j < TK; j += 4) {
       float4 pv[RT];
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
-          if (p != 0.f) {
+          if (!(p < 0.f)) {
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[i][d] = fmaf(p, vv[d], o[i][d]);
           }

@@ -8,7 +8,7 @@ from medusa_head_speculative_02_b200 import api
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
 
 # (tree (K, s, N), query heads per kv-head, dh, dtype)
 KERNELS = {
@@ -18,6 +18,8 @@ KERNELS = {
     "keys64": ((5, 10, 50), 1, 128, BF),
     "keys128": ((5, 10, 50), 2, 128, BF),
     "pair": ((5, 3, 200), 1, 128, BF),
+    "simt64": ((4, 3, 30), 2, 64, BF),
+    "simt_f32": ((5, 3, 40), 1, 128, F32),
 }
 # (kv-heads, prefix): one chunk, chunks that merge in a cluster (bf16, dh = 128,
 # 17 to 128 rows), chunks in the workspace
