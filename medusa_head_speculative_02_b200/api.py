@@ -8,6 +8,7 @@ Every step of the computation runs in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes as C
+from operator import attrgetter
 
 import torch
 
@@ -398,8 +399,9 @@ def medusa_kv_compact(k_cache, v_cache, prefix_len, accept_len, accept_nodes, K:
 # part is most of the time: the checks are one expression per tensor (the
 # message is worked out only on failure), pointers go as integers, and the
 # device is switched only when it is not the current one.
-_I32 = torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_I32, _U8, _BF16 = torch.int32, torch.uint8, torch.bfloat16
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_Tensor = torch.Tensor
 
 
 def _refuse(t, name: str, dtype, shape, dev: int):
@@ -410,7 +412,7 @@ def _refuse(t, name: str, dtype, shape, dev: int):
 def _chk(t, name: str, dtype, shape, dev: int) -> int:
     """Data pointer of a contiguous tensor of this dtype and shape on CUDA
     device `dev`; raises otherwise."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or \
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or \
             t.get_device() != dev or not t.is_contiguous():
         _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
@@ -430,7 +432,7 @@ def _dev(t, name: str) -> int:
 
 def _call(dev: int, fn, where: str, *args) -> None:
     """fn(*args, stream) with device `dev` current, on its current stream."""
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -443,34 +445,47 @@ class PackedCache:
     """A 4-bit KV cache: codes uint8 [B][Hkv][Lcap][dh/2] and (scale, zero)
     bf16 [B][Hkv][Lcap][2] of K and V, or with a leading layer axis.  Wraps
     the caller's tensors; ``PackedCache.empty`` makes zeroed ones (every row
-    then stands for zeros)."""
+    then stands for zeros).  Its tensors and sizes are read-only; a tensor may be
+    given other memory of its own shape, which the calls then use, and a call
+    refuses one whose shape, type, device or strides changed."""
 
-    __slots__ = ("_t", "layers", "B", "Hkv", "Lcap", "dh", "device", "_idx")
-    # read-only: the calls rely on the shapes checked at construction
+    __slots__ = ("_t", "_codes", "_par", "_idx", "_layers", "_B", "_Hkv", "_Lcap", "_dh")
     k_codes = property(lambda self: self._t[0])
     k_par = property(lambda self: self._t[1])
     v_codes = property(lambda self: self._t[2])
     v_par = property(lambda self: self._t[3])
+    layers, B, Hkv, Lcap, dh = (property(attrgetter(n)) for n in
+                                ("_layers", "_B", "_Hkv", "_Lcap", "_dh"))
+    device = property(lambda self: self._t[0].device)
 
     def __init__(self, k_codes, k_par, v_codes, v_par):
         _need(k_codes, "k_codes", torch.uint8)
         shape = tuple(k_codes.shape)
         if len(shape) not in (4, 5):
             raise ValueError("k_codes must be [B][Hkv][Lcap][dh/2] or [layers][B][Hkv][Lcap][dh/2]")
-        self._idx = dev = k_codes.get_device()
-        par = shape[:-1] + (2,)
-        _chk(k_par, "k_par", torch.bfloat16, par, dev)
-        _chk(v_codes, "v_codes", torch.uint8, shape, dev)
-        _chk(v_par, "v_par", torch.bfloat16, par, dev)
+        self._idx = k_codes.get_device()
+        self._codes, self._par = k_codes.shape, torch.Size(shape[:-1] + (2,))
+        self._layers = shape[0] if len(shape) == 5 else None
+        self._B, self._Hkv, self._Lcap = shape[-4:-1]
+        self._dh = 2 * shape[-1]
         self._t = (k_codes, k_par, v_codes, v_par)
-        self.layers = shape[0] if len(shape) == 5 else None
-        self.B, self.Hkv, self.Lcap = shape[-4:-1]
-        self.dh = 2 * shape[-1]
-        self.device = k_codes.device
+        self._ptrs  # checks the tensors
 
     @property
     def _ptrs(self):
-        return [t.data_ptr() for t in self._t]
+        """The tensors' addresses, checked now: a tensor may have been resized or
+        given other memory since."""
+        kc, kp, vc, vp = self._t
+        codes, par, dev = self._codes, self._par, self._idx
+        if kc.shape == codes and kp.shape == par and vc.shape == codes and vp.shape == par and \
+                kc.dtype is vc.dtype is _U8 and kp.dtype is vp.dtype is _BF16 and \
+                kc.get_device() == kp.get_device() == vc.get_device() == vp.get_device() == dev and \
+                kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and \
+                vp.is_contiguous():
+            return kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()
+        return tuple(_chk(t, name, dt, shape, dev) for t, name, dt, shape in  # says which
+                     zip(self._t, ("k_codes", "k_par", "v_codes", "v_par"),
+                         (_U8, _BF16, _U8, _BF16), (codes, par, codes, par)))
 
     @classmethod
     def empty(cls, B: int, Hkv: int, Lcap: int, dh: int, device="cuda", layers=None):
@@ -486,7 +501,7 @@ class PackedCache:
         return PackedCache(self.k_codes[i], self.k_par[i], self.v_codes[i], self.v_par[i])
 
     def _single(self) -> None:
-        if self.layers is not None:
+        if self._layers is not None:
             raise ValueError("this call takes one layer's cache (cache.layer(i))")
 
 
@@ -494,11 +509,11 @@ def medusa_kv_pack(k, v, cache: PackedCache, start, count=None) -> None:
     """Stores K/V rows k, v [B][T][Hkv][dh] in the 4-bit cache: token t <
     count[b] (count None: all T) of sequence b at slot start[b] + t."""
     cache._single()
-    dev, dt, B, T = cache._idx, _dt(k), cache.B, k.shape[1]
-    shape = (B, T, cache.Hkv, cache.dh)
+    dev, dt, B, T = cache._idx, _dt(k), cache._B, k.shape[1]
+    shape = (B, T, cache._Hkv, cache._dh)
     _call(dev, L.lib().medusa_kv_pack, "medusa_kv_pack", _chk(k, "k", k.dtype, shape, dev),
           _chk(v, "v", k.dtype, shape, dev), dt, _chk(start, "start", _I32, (B,), dev),
-          _opt(count, "count", _I32, (B,), dev), B, T, cache.Hkv, cache.dh, cache.Lcap,
+          _opt(count, "count", _I32, (B,), dev), B, T, cache._Hkv, cache._dh, cache._Lcap,
           *cache._ptrs)
 
 
@@ -509,8 +524,8 @@ def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = tor
     cache._single()
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    dev, B, T = cache._idx, cache.B, int(T)
-    shape = (B, T, cache.Hkv, cache.dh)
+    dev, B, T = cache._idx, cache._B, int(T)
+    shape = (B, T, cache._Hkv, cache._dh)
     if out is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
         v = torch.empty(shape, dtype=dtype, device=cache.device)
@@ -518,7 +533,7 @@ def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = tor
         k, v = out
     _call(dev, L.lib().medusa_kv_unpack, "medusa_kv_unpack", *cache._ptrs,
           _chk(start, "start", _I32, (B,), dev), _opt(count, "count", _I32, (B,), dev), B, T,
-          cache.Hkv, cache.dh, cache.Lcap, _DT[dtype], _chk(k, "k", dtype, shape, dev),
+          cache._Hkv, cache._dh, cache._Lcap, _DT[dtype], _chk(k, "k", dtype, shape, dev),
           _chk(v, "v", dtype, shape, dev))
     return k, v
 
@@ -527,15 +542,15 @@ def medusa_kv_compact_packed(cache: PackedCache, prefix_len, accept_len, accept_
                              new_len=None):
     """Compaction of the accepted path in a 4-bit cache (every layer of one
     with a layer axis, in one launch); returns new_len [B]."""
-    dev, B = cache._idx, cache.B
+    dev, B = cache._idx, cache._B
     if new_len is None:
         new_len = torch.empty(B, dtype=_I32, device=cache.device)
     _call(dev, L.lib().medusa_kv_compact_packed, "medusa_kv_compact_packed", *cache._ptrs,
-          1 if cache.layers is None else cache.layers,
+          1 if cache._layers is None else cache._layers,
           _chk(prefix_len, "prefix_len", _I32, (B,), dev),
           _chk(accept_len, "accept_len", _I32, (B,), dev),
-          _chk(accept_nodes, "accept_nodes", _I32, (B, K + 1), dev), B, cache.Hkv, cache.dh,
-          cache.Lcap, K, _chk(new_len, "new_len", _I32, (B,), dev))
+          _chk(accept_nodes, "accept_nodes", _I32, (B, K + 1), dev), B, cache._Hkv, cache._dh,
+          cache._Lcap, K, _chk(new_len, "new_len", _I32, (B,), dev))
     return new_len
 
 
@@ -563,7 +578,7 @@ def _ext_buffers(size, q, tree, Hkv, Lcap, window, sinks, dev, out, ws):
         out = torch.empty_like(q)
     else:
         _chk(out, "out", q.dtype, q.shape, dev)
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         need = size(tree, B, Hq, Hkv, dh, Lcap, q.dtype, window, sinks)
     else:
         with torch.cuda.device(dev):
@@ -602,9 +617,9 @@ def medusa_tree_attention_packed(q, cache: PackedCache, prefix_len, tree: Tree, 
     window and sinks.  A one-node tree is single-token decoding."""
     cache._single()
     dt = _dt(q)
-    dev, Hkv, Lcap = cache._idx, cache.Hkv, cache.Lcap
+    dev, Hkv, Lcap = cache._idx, cache._Hkv, cache._Lcap
     B, N, Hq, dh = q.shape
-    pq = _chk(q, "q", q.dtype, (cache.B, N, Hq, cache.dh), dev)
+    pq = _chk(q, "q", q.dtype, (cache._B, N, Hq, cache._dh), dev)
     out, ws, nws = _ext_buffers(attention_packed_workspace_size, q, tree, Hkv, Lcap, window, sinks,
                                 dev, out, ws)
     _call(dev, L.lib().medusa_tree_attention_packed, "medusa_tree_attention_packed", pq,
