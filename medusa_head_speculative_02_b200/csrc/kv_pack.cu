@@ -183,7 +183,7 @@ __device__ __forceinline__ uint32_t encode(const Raw8<T>& x, uint32_t& par) {
   constexpr bool kFine = sizeof(T) == 2;  // ties made exact
   constexpr float kMagic = 12582912.f;    // 1.5 * 2^23
   constexpr float kFirst = kFine ? 12288.f : kMagic;  // 1.5 * 2^13
-  constexpr int kBits = 0x4b400000;       // kMagic's bits: those of kMagic + n are kBits + n
+  constexpr uint32_t kBits = 0x4b400000u;  // kMagic's bits: those of kMagic + n are kBits + n
   float tz = fmaf(-lo, r, kFirst), th = fmaf(hi, r, kFirst);
   if (kFine) {
     tz = __fadd_rn(tz, kMagic - kFirst);
@@ -191,10 +191,10 @@ __device__ __forceinline__ uint32_t encode(const Raw8<T>& x, uint32_t& par) {
   }
   float zero = __fsub_rn(tz, kMagic);
   float far = fabsf(fmaf(-lo, r, -zero));  // fp32: largest distance from an integer
-  const int bias = __float_as_int(tz) - 2 * kBits;
-  const bool over = __float_as_int(th) + bias > 15;
+  const uint32_t bias = __float_as_uint(tz) - 2u * kBits;  // (modulo 2^32: t[i] + bias is the code)
+  const bool over = __float_as_uint(th) + bias > 15u;
   const unsigned long long r2 = f2_pack(r, r), first2 = f2_pack(kFirst, kFirst);
-  int t[8];
+  uint32_t t[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const unsigned long long x2 = f2_pack(x.get(2 * i), x.get(2 * i + 1));
@@ -208,17 +208,17 @@ __device__ __forceinline__ uint32_t encode(const Raw8<T>& x, uint32_t& par) {
     }
     float t0, t1;
     f2_unpack(t2, t0, t1);
-    t[2 * i] = __float_as_int(t0);
-    t[2 * i + 1] = __float_as_int(t1);
+    t[2 * i] = __float_as_uint(t0);
+    t[2 * i + 1] = __float_as_uint(t1);
   }
   uint32_t w = 0u;
   if (!over) {
 #pragma unroll
-    for (int i = 7; i >= 0; --i) w = w * 16u + (uint32_t)t[i];
-    w += (uint32_t)bias * 0x11111111u;
+    for (int i = 7; i >= 0; --i) w = w * 16u + t[i];
+    w += bias * 0x11111111u;
   } else {
 #pragma unroll
-    for (int i = 7; i >= 0; --i) w = w * 16u + (uint32_t)__viaddmin_s32(t[i], bias, 15);
+    for (int i = 7; i >= 0; --i) w = w * 16u + __viaddmin_u32(t[i], bias, 15u);
   }
   // (1 / s may overflow for the smallest scales; far is the lane's own: every
   // lane of a row finds the same zero either way)
