@@ -47,6 +47,15 @@ def heads_flops(c: MedusaConfig) -> int:
     return 2 * c.B * c.K * (c.d * c.d + c.V * c.d)
 
 
+def visible_prefix(L: int, window: int, sinks: int) -> int:
+    """Prefix slots that some tree node sees: the sinks, and the slots from the
+    root's window start (the root sees furthest back)."""
+    if window <= 0:
+        return L
+    tail = max(0, min(L, L - window + 1))
+    return min(sinks, tail) + L - tail
+
+
 def attention_bytes(c: MedusaConfig, prefix_sum: int) -> int:
     """K and V of every visible slot (prefix and tree) read once, Q read, O written."""
     e = 4 if c.dtype == "f32" else 2

@@ -136,14 +136,19 @@ class VerifyStep:
     def heads_bytes(self) -> int:
         return kernel_bench.heads_bytes(self.cfg)
 
+    def _prefix_sum(self) -> int:
+        """Prefix slots that the attention call has to read, over the sequences."""
+        return sum(kernel_bench.visible_prefix(L, self.window, self.sinks)
+                   for L in self.x["prefix_len"].tolist())
+
     def attention_flops(self) -> int:
         """Tensor-core work of the attention call: S = Q K^T and O = P V over
-        every key of a sequence's prefix and tree slots, per query row."""
-        return kernel_bench.attention_flops(self.cfg, int(self.x["prefix_len"].sum().item()))
+        every key of a sequence's visible prefix and tree slots, per query row."""
+        return kernel_bench.attention_flops(self.cfg, self._prefix_sum())
 
     def attention_bytes(self) -> int:
-        """K/V actually read (prefix + tree slots) + Q + O."""
-        return kernel_bench.attention_bytes(self.cfg, int(self.x["prefix_len"].sum().item()))
+        """K/V actually read (visible prefix + tree slots) + Q + O."""
+        return kernel_bench.attention_bytes(self.cfg, self._prefix_sum())
 
 
 class PackedVerifyStep(VerifyStep):
