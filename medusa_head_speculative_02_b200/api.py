@@ -554,14 +554,21 @@ def medusa_kv_compact_packed(cache: PackedCache, prefix_len, accept_len, accept_
     return new_len
 
 
+def _chk_window(window: int, sinks: int) -> None:
+    if not (0 <= window < 2**31 and 0 <= sinks < 2**31):  # (a C int would wrap)
+        raise ValueError(f"window and sinks must be in [0, 2^31), got {window} and {sinks}")
+
+
 def attention_packed_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
                                     window: int = 0, sinks: int = 0) -> int:
+    _chk_window(window, sinks)
     return L.lib().medusa_tree_attention_packed_workspace_size(
         tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks)
 
 
 def attention_window_workspace_size(tree: Tree, B, Hq, Hkv, dh, Lcap, dtype: torch.dtype,
                                     window: int, sinks: int = 0) -> int:
+    _chk_window(window, sinks)
     return L.lib().medusa_tree_attention_window_workspace_size(
         tree.handle, B, Hq, Hkv, dh, Lcap, _DT[dtype], window, sinks)
 
@@ -572,8 +579,6 @@ def _ext_buffers(size, q, tree, Hkv, Lcap, window, sinks, dev, out, ws):
     B, N, Hq, dh = q.shape
     if N != tree.N:
         raise ValueError(f"q has {N} nodes, tree has {tree.N}")
-    if not (0 <= window < 2**31 and 0 <= sinks < 2**31):  # (a C int would wrap)
-        raise ValueError(f"window and sinks must be in [0, 2^31), got {window} and {sinks}")
     if out is None:
         out = torch.empty_like(q)
     else:
