@@ -16,9 +16,10 @@ from . import api, kernel_bench
 from .synthetic import MedusaConfig, gen_inputs, plant_verify_logits
 
 # kernels this library launches per call
-# (heads: stage-1 GEMM, SiLU epilogue, stage-2 GEMM, top-s merge; attention:
-# one or two, asked of the library, see launches_per_step)
-LAUNCHES = {"heads": 4, "build_tree": 1, "accept": 2, "kv_compact": 1}
+# (heads, bf16: stage-1 GEMM, SiLU epilogue, stage-2 GEMM, top-s merge; fp32:
+# stage 1 with its epilogue, stage 2, top-s; attention: one or two, asked of the
+# library, see launches_per_step)
+LAUNCHES = {"heads": {"bf16": 4, "f32": 3}, "build_tree": 1, "accept": 2, "kv_compact": 1}
 
 
 class VerifyStep:
@@ -130,7 +131,7 @@ class VerifyStep:
             attn = 1 + (self._attention_workspace() > 0)
         else:
             attn = api.attention_launches(self.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap, c.torch_dtype)
-        return (LAUNCHES["heads"] + LAUNCHES["build_tree"] + attn + acc + LAUNCHES["kv_compact"])
+        return (LAUNCHES["heads"][c.dtype] + LAUNCHES["build_tree"] + attn + acc + LAUNCHES["kv_compact"])
 
     # algorithmic work ---------------------------------------------------------
     def heads_bytes(self) -> int:
@@ -203,9 +204,10 @@ class PackedVerifyStep(VerifyStep):
         self.compact()
 
     def launches_per_step(self) -> int:
-        acc = LAUNCHES["accept"] + 1 if self.cfg.accept == "both" else LAUNCHES["accept"]
+        c = self.cfg
+        acc = LAUNCHES["accept"] + 1 if c.accept == "both" else LAUNCHES["accept"]
         attn = 1 + (self._attention_workspace() > 0)  # a second kernel merges key chunks
-        return (LAUNCHES["heads"] + LAUNCHES["build_tree"] + 1 + attn + acc + LAUNCHES["kv_compact"])
+        return (LAUNCHES["heads"][c.dtype] + LAUNCHES["build_tree"] + 1 + attn + acc + LAUNCHES["kv_compact"])
 
     def attention_bytes(self) -> int:
         raise NotImplementedError("counted for the bf16/fp32 cache only")
@@ -258,7 +260,7 @@ class MultiLayerStep:
         c = self.st.cfg
         attn = api.attention_launches(self.st.tree, c.B, c.Hq, c.Hkv, c.dh, c.Lcap, c.torch_dtype)
         acc = LAUNCHES["accept"] + 1 if c.accept == "both" else LAUNCHES["accept"]
-        return (LAUNCHES["heads"] + LAUNCHES["build_tree"] + self.layers * attn + acc +
+        return (LAUNCHES["heads"][c.dtype] + LAUNCHES["build_tree"] + self.layers * attn + acc +
                 LAUNCHES["kv_compact"])
 
 
