@@ -104,6 +104,9 @@ int medusa_device_status(int* status, int clear);
  * launch fails; asynchronous otherwise.
  */
 int medusa_selftest_wait_timeout(int limit_ms, void* stream);
+/* The same in the source of the tcgen05 4-bit attention kernels, which keeps
+ * status words of its own; medusa_device_status reads and clears them too. */
+int medusa_selftest_wait_timeout_packed(int limit_ms, void* stream);
 
 /* ------------------------------------------------------------------------
  * Tree plan.  [MD] "ツリーアテンションによる並列検証": each of the K heads

@@ -60,12 +60,13 @@ def device_status(clear: bool = True) -> int:
     return st.value
 
 
-def selftest_wait_timeout(limit_ms: int, device=None) -> None:
+def selftest_wait_timeout(limit_ms: int, device=None, packed: bool = False) -> None:
     """Launch the library's bounded-wait self-test on the current stream: one
     thread waits for a barrier phase that nothing completes, gives up after
-    limit_ms, raises the device status word and returns."""
-    L.check(L.lib().medusa_selftest_wait_timeout(int(limit_ms), _stream(device)),
-            "medusa_selftest_wait_timeout")
+    limit_ms, raises the device status word (packed: that of the 4-bit
+    attention kernels, which have their own) and returns."""
+    name = "medusa_selftest_wait_timeout" + ("_packed" if packed else "")
+    L.check(getattr(L.lib(), name)(int(limit_ms), _stream(device)), name)
 
 
 def tree_plan_host(K: int, s: int, N: int):

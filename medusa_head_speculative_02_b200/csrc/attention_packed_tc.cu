@@ -993,6 +993,27 @@ int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear) {
 }
 
 namespace {
+// One thread waits for phase 0 of a barrier that no thread arrives at.
+__global__ void packed_selftest_wait_kernel(unsigned long long limit_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait_limit(&bar, 0u, &abort_flag, limit_ns);
+}
+}  // namespace
+
+int attention_packed_tc_selftest(unsigned long long limit_ns, cudaStream_t st) {
+  packed_selftest_wait_kernel<<<1, 32, 0, st>>>(limit_ns);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "packed_selftest_wait_kernel launch");
+}
+
+namespace {
 int pair_run(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& kp,
              const CUtensorMap& vp, const PackedParams& p, long long ctas, cudaStream_t st) {
   static std::atomic<bool> done[64];

@@ -197,7 +197,9 @@ struct AttnExtArgs {
 bool attention_packed_tc_eligible(int dtype, int dh);
 size_t attention_packed_tc_workspace(const medusa_tree* t, int B, int Hq, int Hkv, int Lcap,
                                      int window, int sinks);
+// that source's status words, and a bounded wait of its own that runs out
 int attention_packed_tc_status(unsigned* status, unsigned* site, bool clear);
+int attention_packed_tc_selftest(unsigned long long limit_ns, cudaStream_t st);
 int attention_packed_tc_launch(const AttnArgs& a, const PackedCache& c, cudaStream_t st);
 // the same for at most 16 query rows per kv-head (csrc/attention_packed_rows.cu)
 bool attention_packed_rows_eligible(int dtype, int dh, int rows);

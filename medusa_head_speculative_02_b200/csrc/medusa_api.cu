@@ -267,6 +267,13 @@ int medusa_selftest_wait_timeout(int limit_ms, void* stream) {
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail(e, "selftest_wait_kernel launch");
 }
 
+int medusa_selftest_wait_timeout_packed(int limit_ms, void* stream) {
+  if (limit_ms < 1 || limit_ms > 2000)
+    return fail(MEDUSA_ERR_INVALID_ARG, "limit_ms must be in [1, 2000]");
+  return attention_packed_tc_selftest((unsigned long long)limit_ms * 1000000ull,
+                                      (cudaStream_t)stream);
+}
+
 const char* medusa_last_error(void) { return t_last_error.c_str(); }
 
 #ifdef MEDUSA_DEBUG
