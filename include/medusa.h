@@ -395,7 +395,8 @@ int medusa_kv_compact_layers(void* k_caches, void* v_caches, int n_layers,
  * cache that a step reads.
  * window >= 0, 0 = no window (then sinks is ignored); sinks >= 0.  A node
  * always sees itself.  Layouts, dtypes, limits and errors are those of
- * medusa_tree_attention.  Slots that some node sees must hold finite values;
+ * medusa_tree_attention, and Lcap < 2^31 - 1024 (else UNSUPPORTED).  Slots
+ * that some node sees must hold finite values;
  * all others (slots that have left every window, unused capacity) may hold
  * anything.  Only the key tiles with a visible slot are read.
  * A sequence with L_b < 0 or L_b + N > Lcap gets rows of zeros.
@@ -466,7 +467,8 @@ int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_
  * single-token decoding.  Only the key tiles with a visible slot are read.
  * A visible row with scale NaN makes the output of the nodes that see it NaN;
  * slots that no node sees may hold anything.  A sequence with L_b < 0 or
- * L_b + N > Lcap gets rows of zeros.  q finite.
+ * L_b + N > Lcap gets rows of zeros.  q finite.  Lcap < 2^31 - 1024 (else
+ * UNSUPPORTED).
  * bf16 with dh = 128 runs on the tensor cores, by the query rows per kv-head
  * R = N Hq/Hkv (any Hq/Hkv):
  *   R <= 16   mma.sync, a warp per 16-key group; codes exact in fp16

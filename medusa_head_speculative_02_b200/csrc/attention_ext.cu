@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_ext_simt_kernel(const Simt
   int per = (vr.total + a.P - 1) / a.P;
   per = (per + TK - 1) / TK * TK;
   const int u_lo = (int)min((long long)vr.total, (long long)chunk * per);
-  const int u_hi = min(vr.total, u_lo + per);
+  const int u_hi = (int)min((long long)vr.total, (long long)u_lo + per);
 
   float m[RT], l[RT], o[RT][DT];
 #pragma unroll

@@ -679,6 +679,8 @@ int check_attention_ext(const medusa_tree_t* tree, int B, int Hq, int Hkv, int d
   if (dh != 64 && dh != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "dh must be 64 or 128");
   if (Lcap < tree->N) return fail(MEDUSA_ERR_INVALID_ARG, "Lcap < N");
   if (packed && Lcap % 4) return fail(MEDUSA_ERR_UNSUPPORTED, "4-bit cache: Lcap must be a multiple of 4");
+  // slots rounded up to whole tiles and chunks stay in 31 bits
+  if (Lcap > 0x7fffffff - 1024) return fail(MEDUSA_ERR_UNSUPPORTED, "Lcap above 2^31 - 1025");
   if (window < 0 || sinks < 0) return fail(MEDUSA_ERR_INVALID_ARG, "window and sinks must be >= 0");
   // query rows of the call, and of one kv-head's partial rows, in 31 bits
   if ((long long)B * tree->N * Hq > 0x7fffffffLL)
