@@ -419,10 +419,6 @@ def _chk(t, name: str, dtype, shape, dev: int) -> int:
     return t.data_ptr()
 
 
-def _opt(t, name: str, dtype, shape, dev: int):
-    return None if t is None else _chk(t, name, dtype, shape, dev)
-
-
 def _dev(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
@@ -431,13 +427,13 @@ def _dev(t, name: str) -> int:
     return t.get_device()
 
 
-def _call(dev: int, fn, where: str, *args) -> None:
-    """fn(*args, stream) with device `dev` current, on its current stream."""
+def _call(dev: int, fn, where: str, args: tuple) -> None:
+    """fn(*args) with device `dev` current; the last argument is its stream."""
     if _current_device() == dev:
-        rc = fn(*args, _raw_stream(dev))
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev))
+            rc = fn(*args)
     if rc:
         L.check(rc, where)
 
@@ -450,21 +446,21 @@ class PackedCache:
     given other memory of its own shape, which the calls then use, and a call
     refuses one whose shape, type, device or strides changed."""
 
-    __slots__ = ("_t", "_codes", "_par", "_idx", "_layers", "_B", "_Hkv", "_Lcap", "_dh")
+    __slots__ = ("_t", "_codes", "_par", "_idx", "_layers", "_B", "_Hkv", "_Lcap", "_dh",
+                 "_device")
     k_codes = property(lambda self: self._t[0])
     k_par = property(lambda self: self._t[1])
     v_codes = property(lambda self: self._t[2])
     v_par = property(lambda self: self._t[3])
-    layers, B, Hkv, Lcap, dh = (property(attrgetter(n)) for n in
-                                ("_layers", "_B", "_Hkv", "_Lcap", "_dh"))
-    device = property(lambda self: self._t[0].device)
+    layers, B, Hkv, Lcap, dh, device = (
+        property(attrgetter(n)) for n in ("_layers", "_B", "_Hkv", "_Lcap", "_dh", "_device"))
 
     def __init__(self, k_codes, k_par, v_codes, v_par):
         _need(k_codes, "k_codes", torch.uint8)
         shape = tuple(k_codes.shape)
         if len(shape) not in (4, 5):
             raise ValueError("k_codes must be [B][Hkv][Lcap][dh/2] or [layers][B][Hkv][Lcap][dh/2]")
-        self._idx = k_codes.get_device()
+        self._idx, self._device = k_codes.get_device(), k_codes.device
         self._codes, self._par = k_codes.shape, torch.Size(shape[:-1] + (2,))
         self._layers = shape[0] if len(shape) == 5 else None
         self._B, self._Hkv, self._Lcap = shape[-4:-1]
@@ -512,10 +508,11 @@ def medusa_kv_pack(k, v, cache: PackedCache, start, count=None) -> None:
     cache._single()
     dev, dt, B, T = cache._idx, _dt(k), cache._B, k.shape[1]
     shape = (B, T, cache._Hkv, cache._dh)
-    _call(dev, L.lib().medusa_kv_pack, "medusa_kv_pack", _chk(k, "k", k.dtype, shape, dev),
-          _chk(v, "v", k.dtype, shape, dev), dt, _chk(start, "start", _I32, (B,), dev),
-          _opt(count, "count", _I32, (B,), dev), B, T, cache._Hkv, cache._dh, cache._Lcap,
-          *cache._ptrs)
+    _call(dev, L.lib().medusa_kv_pack, "medusa_kv_pack",
+          (_chk(k, "k", k.dtype, shape, dev), _chk(v, "v", k.dtype, shape, dev), dt,
+           _chk(start, "start", _I32, (B,), dev),
+           None if count is None else _chk(count, "count", _I32, (B,), dev), B, T, cache._Hkv,
+           cache._dh, cache._Lcap, *cache._ptrs, _raw_stream(dev)))
 
 
 def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = torch.bfloat16,
@@ -528,14 +525,16 @@ def medusa_kv_unpack(cache: PackedCache, start, T: int, dtype: torch.dtype = tor
     dev, B, T = cache._idx, cache._B, int(T)
     shape = (B, T, cache._Hkv, cache._dh)
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = torch.empty(shape, dtype=dtype, device=cache._device)
+        v = torch.empty(shape, dtype=dtype, device=cache._device)
+        pk, pv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
-    _call(dev, L.lib().medusa_kv_unpack, "medusa_kv_unpack", *cache._ptrs,
-          _chk(start, "start", _I32, (B,), dev), _opt(count, "count", _I32, (B,), dev), B, T,
-          cache._Hkv, cache._dh, cache._Lcap, _DT[dtype], _chk(k, "k", dtype, shape, dev),
-          _chk(v, "v", dtype, shape, dev))
+        pk, pv = _chk(k, "k", dtype, shape, dev), _chk(v, "v", dtype, shape, dev)
+    _call(dev, L.lib().medusa_kv_unpack, "medusa_kv_unpack",
+          (*cache._ptrs, _chk(start, "start", _I32, (B,), dev),
+           None if count is None else _chk(count, "count", _I32, (B,), dev), B, T, cache._Hkv,
+           cache._dh, cache._Lcap, _DT[dtype], pk, pv, _raw_stream(dev)))
     return k, v
 
 
@@ -545,13 +544,16 @@ def medusa_kv_compact_packed(cache: PackedCache, prefix_len, accept_len, accept_
     with a layer axis, in one launch); returns new_len [B]."""
     dev, B = cache._idx, cache._B
     if new_len is None:
-        new_len = torch.empty(B, dtype=_I32, device=cache.device)
-    _call(dev, L.lib().medusa_kv_compact_packed, "medusa_kv_compact_packed", *cache._ptrs,
-          1 if cache._layers is None else cache._layers,
-          _chk(prefix_len, "prefix_len", _I32, (B,), dev),
-          _chk(accept_len, "accept_len", _I32, (B,), dev),
-          _chk(accept_nodes, "accept_nodes", _I32, (B, K + 1), dev), B, cache._Hkv, cache._dh,
-          cache._Lcap, K, _chk(new_len, "new_len", _I32, (B,), dev))
+        new_len = torch.empty(B, dtype=_I32, device=cache._device)
+        pn = new_len.data_ptr()
+    else:
+        pn = _chk(new_len, "new_len", _I32, (B,), dev)
+    _call(dev, L.lib().medusa_kv_compact_packed, "medusa_kv_compact_packed",
+          (*cache._ptrs, 1 if cache._layers is None else cache._layers,
+           _chk(prefix_len, "prefix_len", _I32, (B,), dev),
+           _chk(accept_len, "accept_len", _I32, (B,), dev),
+           _chk(accept_nodes, "accept_nodes", _I32, (B, K + 1), dev), B, cache._Hkv, cache._dh,
+           cache._Lcap, K, pn, _raw_stream(dev)))
     return new_len
 
 
@@ -610,10 +612,10 @@ def medusa_tree_attention_window(q, k_cache, v_cache, prefix_len, tree: Tree, sc
     out, ws, nws = _ext_buffers(attention_window_workspace_size, q, tree, Hkv, Lcap, window, sinks,
                                 dev, out, ws)
     _call(dev, L.lib().medusa_tree_attention_window, "medusa_tree_attention_window",
-          _chk(q, "q", q.dtype, q.shape, dev), _chk(k_cache, "k_cache", q.dtype, shape, dev),
-          _chk(v_cache, "v_cache", q.dtype, shape, dev),
-          _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq, Hkv, dh, Lcap,
-          scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws)
+          (_chk(q, "q", q.dtype, q.shape, dev), _chk(k_cache, "k_cache", q.dtype, shape, dev),
+           _chk(v_cache, "v_cache", q.dtype, shape, dev),
+           _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq, Hkv, dh, Lcap,
+           scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws, _raw_stream(dev)))
     return out
 
 
@@ -628,7 +630,8 @@ def medusa_tree_attention_packed(q, cache: PackedCache, prefix_len, tree: Tree, 
     pq = _chk(q, "q", q.dtype, (cache._B, N, Hq, cache._dh), dev)
     out, ws, nws = _ext_buffers(attention_packed_workspace_size, q, tree, Hkv, Lcap, window, sinks,
                                 dev, out, ws)
-    _call(dev, L.lib().medusa_tree_attention_packed, "medusa_tree_attention_packed", pq,
-          *cache._ptrs, _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq, Hkv,
-          dh, Lcap, scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws)
+    _call(dev, L.lib().medusa_tree_attention_packed, "medusa_tree_attention_packed",
+          (pq, *cache._ptrs, _chk(prefix_len, "prefix_len", _I32, (B,), dev), tree.handle, B, Hq,
+           Hkv, dh, Lcap, scale, dt, window, sinks, out.data_ptr(), ws.data_ptr(), nws,
+           _raw_stream(dev)))
     return out
