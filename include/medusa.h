@@ -453,7 +453,7 @@ int medusa_kv_unpack(const void* k_codes, const void* k_par, const void* v_codes
  * layers' arrays follow one another: *_codes [n_layers][B][Hkv][Lcap][dh/2],
  * *_par [n_layers][B][Hkv][Lcap][2].  Rows move bit for bit; new_len [B] (may
  * be NULL; an array of its own, not prefix_len or accept_len) as
- * medusa_kv_compact writes it; same skipped entries.
+ * medusa_kv_compact writes it, also for n_layers = 0; same skipped entries.
  */
 int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_par, int n_layers,
                              const int32_t* prefix_len, const int32_t* accept_len,

@@ -819,14 +819,16 @@ int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_
   int rc = check_packed_shape(B, 0, Hkv, dh, Lcap);
   if (rc) return rc;
   if (n_layers < 0 || K < 0 || K > MEDUSA_MAX_K) return fail(MEDUSA_ERR_INVALID_ARG, "bad shape");
-  if (B == 0 || n_layers == 0) return MEDUSA_OK;
+  if (B == 0 || (n_layers == 0 && !new_len)) return MEDUSA_OK;
   if (!prefix_len || !accept_len || !accept_nodes)
     return fail(MEDUSA_ERR_INVALID_ARG, "NULL pointer");
   // other threads still read the lengths when new_len is written
   if (new_len && (new_len == prefix_len || new_len == accept_len))
     return fail(MEDUSA_ERR_INVALID_ARG, "new_len must be an array of its own");
-  rc = check_packed(k_codes, k_par, v_codes, v_par);
-  if (rc) return rc;
+  if (n_layers > 0) {  // (without layers only new_len is written)
+    rc = check_packed(k_codes, k_par, v_codes, v_par);
+    if (rc) return rc;
+  }
   return kv_compact_packed_launch({k_codes, k_par, v_codes, v_par, Hkv, dh, Lcap}, n_layers, B,
                                   prefix_len, accept_len, accept_nodes, K, new_len,
                                   (cudaStream_t)stream);
