@@ -478,9 +478,11 @@ int medusa_kv_compact_packed(void* k_codes, void* k_par, void* v_codes, void* v_
  * Scores, softmax statistics, sums and products are fp32.  Softmax weights
  * (in the first two kernels times the value scale) are rounded once to fp16,
  * relative to the row's maximum (and to the largest value scale): below 2^-21
- * they lose bits, below 2^-32 they count as 0.  In the last kernel so do K and
- * V rows whose scale is below 2^-20 of the largest of their 128 keys (K) or of
- * the keys so far (V).  Queries are held in fp16 under one power of two for at
+ * they lose bits, below 2^-32 they count as 0 (but 0 x NaN is NaN).  The last
+ * kernel rounds the weights of 64 keys twice where the next 64 raise the
+ * maximum by more than 2^8, and K and V rows lose bits there whose scale is
+ * below 2^-20 of the largest of their 128 keys (K) or of the keys so far (V).
+ * Queries are held in fp16 under one power of two for at
  * most 256 query rows of a kv-head: elements below 2^-26 of the largest lose
  * bits.  |q| and the row scales stay below 2^100.
  * fp32, and dh = 64, run on a SIMT kernel in fp32.

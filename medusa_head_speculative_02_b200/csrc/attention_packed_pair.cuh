@@ -17,9 +17,11 @@
 // PV_a(t), S_a(t+1), PV_b(t), S_b(t+1): one tile's products run during the
 // other's softmax.  K and V are unpacked with their scales, relative to a power
 // of two >= the tile's largest for K (one factor on the tile's scores) and >=
-// the largest so far for V (its growth rescales O), and rounded once to fp16:
-// scales read from shared memory by every softmax thread (128 a tile) made the
-// call 1.25 x as long.  A row whose K or V has no finite scale is stored as 0
+// the largest so far for V (its growth rescales O), 2^-117 at least, and rounded
+// once to fp16 (scales read from shared memory by every softmax thread, 128 a
+// tile, made the call 1.25 x as long).  The weights of a tile's first 64 keys are
+// rounded to fp16 a second time when the other 64 raise the row's maximum by
+// more than 2^8.  A row whose K or V has no finite scale is stored as 0
 // and put back as NaN scores, so that it reaches the rows that see it only.
 // Warpgroups: 0 TMA (ring of K and V code tiles) and MMA issue, 1 unpack, 2
 // and 3 the softmax of query tiles a and b.

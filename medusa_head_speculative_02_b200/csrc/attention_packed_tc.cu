@@ -33,9 +33,10 @@
 //
 // What bounds it (64-node trees): the chain products -> softmax -> products of
 // a tile, and per tile and softmax thread the 16 to 64 rows' multiply-add,
-// exponential and rounding.  64 rows, 37 heads x 4 sequences of 8K: 104 us;
-// 64 rows, 32 heads, 2K prefix (the 7B verify step): 21.1 us launch to launch,
-// against a cache of 1.6 us of HBM time.
+// exponential and rounding.  64 rows, 37 heads x 4 sequences of 8K: 104 us of 26
+// at the HBM rate, one wave of 148 CTAs with 65 tiles each; 40 heads x 8
+// sequences of 1K to 4K: 125 us of 19; 64 rows, 32 heads, 2K prefix (the 7B
+// verify step): 20.9 us launch to launch, against a cache of 1.6 us of HBM time.
 //
 // Key chunks fill the GPU when there are few (sequence, kv-head) pairs; up to 8
 // of them form a cluster and merge through distributed shared memory when all
@@ -45,7 +46,8 @@
 // TMEM: O^T, two S^T buffers, two K buffers.
 // This source is compiled without relocatable device code: register splits
 // between warpgroups (setmaxnreg) are only honoured then, and without them the
-// softmax threads' 64 rows would spill.
+// softmax threads' 64 rows would spill.  (With 128 columns 20 bytes a thread
+// still do; 32 and 64 columns spill nothing.)
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 

@@ -52,9 +52,10 @@
 // everything between is never read.  Work per step is then bounded by the
 // window: 64-node trees, 32 heads, 2048-token prefix, window 512: 6 key tiles
 // per kv-head instead of 17 (14 us, of them 12 start-up, merge and launch); 4 x
-// 32K, 52 heads, 256-node trees, window 4096: 170 us of 75 at the HBM rate (the
-// whole prefix 1.0 ms), bound by the same waits as without a window; 16 single
-// tokens, 8 kv-heads, window 4095: 58 us of 41.
+// 32K, 52 heads, 256-node trees, window 4096: 197 us in a row of calls (171 in 30
+// calls, before the power cap) of 75 at the HBM rate (the whole prefix 1.0 ms),
+// bound by the same waits as without a window and the start and end of each CTA;
+// 16 single tokens, 8 kv-heads, prefixes of 1 to 8192, window 4095: 54-62 us of 31.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -1260,9 +1261,9 @@ TcShape attention_tc_shape(int B, int Hq, int Hkv, int N, int Lcap, bool window)
   const long long T = (Lcap - N + BN - 1) / BN + (N + BN - 1) / BN;
   // With a window a CTA has few tiles, and its start and end count: about 8
   // tiles' time with one query tile (14 with chunks to merge), 6.5 with two (10.5
-  // with the merge).  52 heads, 256-node trees: 2 sequences, window 1024 and
-  // 4096, 75 and 125 us without it and 43 and 102 with it; 4 sequences 112 and
-  // 199, 76 and 170.  (Counted twice below, to stay in integers.)
+  // with the merge).  52 heads, 256-node trees (30 calls each): 2 sequences, window
+  // 1024 and 4096, 75 and 125 us without it and 43 and 102 with it; 4 sequences
+  // 112 and 199, 76 and 170.  (Counted twice below, to stay in integers.)
   const long long end1 = !window ? 0 : sh.P > 1 ? 28 : 16;
   const long long cost1 =
       ((units * sh.P + sms - 1) / sms) * (2 * ((T + sh.P - 1) / sh.P) + end1);
